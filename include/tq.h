@@ -274,6 +274,94 @@ TQ_API tq_status tq_prefill_attention(const tq_ctx* ctx, const uint16_t* q_dev, 
                                       int max_blocks, int q_start, int Tq, int Hq, int Hkv, float scale, void* out_dev,
                                       int out_fp32, void* stream);
 
+/* Rotary layouts and scalings (tq_rope_plan). */
+typedef enum { TQ_ROPE_HALF = 0, TQ_ROPE_INTERLEAVED = 1 } tq_rope_layout;
+typedef enum {
+    TQ_ROPE_SCALE_NONE = 0,
+    TQ_ROPE_SCALE_LINEAR = 1,  /* positions interpolated: theta / factor */
+    TQ_ROPE_SCALE_NTK = 2,     /* base * factor^(rot / (rot - 2)) */
+    TQ_ROPE_SCALE_BANDS = 3,   /* theta / factor for long wavelengths, theta for short ones */
+    TQ_ROPE_SCALE_YARN = 4     /* a linear ramp between the two over the pairs, and a factor on the values */
+} tq_rope_scaling;
+
+/* Frequencies of a rotary embedding, filled by tq_rope_plan; plain data that the caller
+ * may copy (it holds no pointers). */
+typedef struct {
+    int32_t rot_dim;     /* rotated coordinates of a head: its first rot_dim */
+    int32_t layout;      /* tq_rope_layout */
+    float mscale;        /* factor on the rotated coordinates (1 but for TQ_ROPE_SCALE_YARN) */
+    int32_t reserved;
+    uint64_t turns[64];  /* theta_i / (2 pi) of pair i in units of 2^-64 turns a position */
+} tq_rope_table;
+
+/*
+ * tq_rope_plan -- the frequencies of a rotary position embedding, on the host.  Pair i
+ * (i < rot/2) turns by pos * theta_i, theta_i = base^(-2 i / rot), changed by the scaling:
+ *   NONE    nothing; factor, original_len, low and high are not looked at.
+ *   LINEAR  theta / factor.
+ *   NTK     theta of the base `base * factor^(rot / (rot - 2))` (rot_dim > 2).
+ *   BANDS   with keep = clamp((original_len / wavelength - low) / (high - low), 0, 1),
+ *           wavelength = 2 pi / theta:  theta (keep + (1 - keep) / factor); low < high.
+ *   YARN    [Peng et al., "YaRN: Efficient Context Window Extension of Large Language
+ *           Models", 2023] with at(beta) = rot ln(original_len / (2 pi beta)) / (2 ln base),
+ *           first = max(floor(at(high)), 0), last = min(ceil(at(low)), rot - 1) and
+ *           ramp = clamp((i - first) / max(last - first, 0.001), 0, 1):
+ *           theta (1 - ramp + ramp / factor), mscale = 0.1 ln(factor) + 1; low < high.
+ *   rot_dim : 2 .. 128, even.   layout : HALF pairs (i, i + rot/2); INTERLEAVED (2i, 2i+1).
+ *   base    : > 1, finite.      factor : >= 1, finite.   original_len, low, high : > 0.
+ * TQ_ERR_INVALID_ARG on anything else, TQ_ERR_UNSUPPORTED on an unknown layout or scaling.
+ */
+TQ_API tq_status tq_rope_plan(int rot_dim, int layout, double base, int scaling, double factor, double original_len,
+                              double low, double high, tq_rope_table* out);
+
+/*
+ * tq_rope -- rotary positions of a batch of queries and keys, in one kernel launch:
+ *   (x1, x2) of pair i -> mscale (x1 cos a - x2 sin a, x2 cos a + x1 sin a), a = pos theta_i
+ * in fp32, rounded once; coordinates from rot_dim on are copied.  transpose != 0 applies
+ * the transposed map (-a instead of a): the gradient with respect to the inputs given the
+ * gradient of the outputs, and for mscale = 1 the inverse.
+ *   q_dev, k_dev : fp16 rows of Hq (Hkv) heads of 128, q_stride (k_stride) elements from one
+ *                  token to the next (a multiple of 8, >= heads * 128): views into a fused
+ *                  projection work as they are.  Either may be NULL (its heads are then not
+ *                  looked at).  16-byte aligned.
+ *   positions_dev: [T] int32; a negative position leaves the token's rows as they are (the
+ *                  output's, if that is another buffer).  Any int32 position is exact to
+ *                  2^-32 turns.
+ *   q_out, k_out : as the inputs, with strides of their own.  An output may be its own
+ *                  input (same address and stride); any other overlap among the inputs and
+ *                  outputs is refused.
+ * Needs no context: the current device must be the pointers'.  T = 0 launches nothing.
+ */
+TQ_API tq_status tq_rope(const tq_rope_table* table, const uint16_t* q_dev, int64_t q_stride, const uint16_t* k_dev,
+                         int64_t k_stride, int T, int Hq, int Hkv, const int32_t* positions_dev, uint16_t* q_out_dev,
+                         int64_t q_out_stride, uint16_t* k_out_dev, int64_t k_out_stride, int transpose,
+                         void* stream);
+
+/*
+ * tq_prompt_attention -- causal attention over whole prompts, packed one behind the other,
+ * on their exact fp16 keys and values (tq_compress takes the same tensors for the steps
+ * that follow).  Query i of sequence b attends to the tokens 0 .. i of the same sequence:
+ *   s_j = scale * <q_i, k_j>,   o_i = sum_{j <= i} softmax(s)_j v_j.
+ *   q_dev, k_dev, v_dev : fp16 rows of Hq (q) and Hkv (k, v) heads of 128, *_stride elements
+ *                  from one token to the next (a multiple of 8, >= heads * 128), 16-byte
+ *                  aligned.
+ *   cu_seqlens_dev : [B + 1] int32, non-decreasing, 0 .. T: sequence b is the rows
+ *                  cu_seqlens[b] .. cu_seqlens[b + 1] - 1 (none is allowed).  A list that is
+ *                  not sets TQ_DEVERR_SEQLEN and leaves rows unwritten; nothing out of range
+ *                  is touched.
+ *   Hq / Hkv     : 1 .. 128.
+ *   scale        : softmax scale; 0 for the default 1/sqrt(d).
+ *   out_dev      : [T][Hq][128], fp16 (out_fp32 = 0) or fp32 (out_fp32 = 1); rows that are in
+ *                  no sequence are left as they were.  Must not overlap the inputs.
+ * Masked tokens are not looked at: whatever they hold (infinities, NaN) reaches no other
+ * query.  One kernel launch on the context's device, no workspace; T = 0 or B = 0 launches
+ * nothing.
+ */
+TQ_API tq_status tq_prompt_attention(const tq_ctx* ctx, const uint16_t* q_dev, int64_t q_stride,
+                                     const uint16_t* k_dev, int64_t k_stride, const uint16_t* v_dev, int64_t v_stride,
+                                     int T, const int32_t* cu_seqlens_dev, int B, int Hq, int Hkv, float scale,
+                                     void* out_dev, int out_fp32, void* stream);
+
 /*
  * Size of the device array behind tq_decode_attention_noalloc.  Every GPU that
  * loads libtq reserves this much device memory for it until the process exits.

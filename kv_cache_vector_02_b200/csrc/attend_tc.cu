@@ -1,0 +1,541 @@
+// Causal attention of ragged sequences over fp16 keys and values on the sm_100a tensor
+// cores (tcgen05 + TMEM + TMA): the kernel behind tq_prompt_attention (the prompt's own
+// keys and values) and, over decompressed pages, behind long chunks of tq_chunk_attention.
+//
+//   s_ij = scale <q_i, k_j>,   o_i = sum_j softmax(s_i)_j v_j,   j <= off + i,
+// off = tokens before the sequence's first query (0 for a whole prompt).
+//
+// One CTA per (256 rows, kv head).  A row is a (query, query head of the group) pair, the
+// group's G heads packed beside each other, so keys and values are read once for all of
+// them and a causal tile's waste is that of 128 / G queries, not of 128.  The rows are two
+// halves of 128 (one TMEM lane each); the halves take turns, one half's softmax running
+// while the tensor core works for the other:
+//   warps 0-3, 4-7  softmax of half 0, 1: one thread per row.  Scores come from tensor
+//                   memory into registers, the running maximum and sum are fp32, base 2;
+//                   P goes back over the scores' own columns as packed fp16
+//   warp 8          MMA issuer (one thread): S = Q K^T (A, B in shared memory),
+//                   O += P V (A in tensor memory, V as it lies: N-major descriptor)
+//   warp 9          TMA producer: Q once, then rings of K and V tiles of 128 tokens
+//   warps 10, 11    masked tiles only: clear what is not finite in V (below)
+// O is rescaled only when a row's maximum has grown by more than 2^8 since the one it is
+// scaled by: P stays below 2^8, far inside fp16, and the sum is exact about it either way.
+//
+// Masked places may hold anything.  Scores are masked by position, whatever their value.
+// P there is 0, but 0 * inf or 0 * NaN in V would reach O: tiles with a masked (row,
+// token) pair are first looked through by warps 10 and 11, which clear non-finite values
+// in shared memory and note it; a row's epilogue then adds those values back (v * p is v
+// for p > 0 and v infinite or NaN) for the tokens the row does attend.
+#include <cuda.h>
+
+#include "device_util.cuh"
+#include "sm100.cuh"
+
+namespace tq {
+namespace {
+
+using namespace sm100;
+
+constexpr int kAN = 128;                    // tokens of a tile
+constexpr uint32_t kATile = 128 * kDim * 2;  // one 128 x 128 fp16 operand
+constexpr uint32_t kAHalf = kATile / 2;      // 64 of its columns
+constexpr int kAKStages = 3, kAVStages = 2;
+constexpr int kAThreads = 384;
+constexpr uint32_t kAOffQ = 0;
+constexpr uint32_t kAOffK = 2 * kATile;
+constexpr uint32_t kAOffV = kAOffK + kAKStages * kATile;
+constexpr uint32_t kAOffBar = kAOffV + kAVStages * kATile;
+constexpr uint32_t kASmem = kAOffBar + 512;
+constexpr uint64_t kAWaitNs = 2000000000ull;
+constexpr float kRescale = 8.f;              // log2 of what P may grow to before O is rescaled
+static_assert(kASmem <= 232448, "shared memory budget");
+
+enum : int {
+    kABQ = 0,
+    kABKFull = 1,    // +stage
+    kABKEmpty = 4,   // +stage
+    kABVFull = 7,    // +stage
+    kABVEmpty = 9,   // +stage
+    kABVClean = 11,  // +stage: a masked tile has been looked through
+    kABS = 13,       // +half: scores in tensor memory (and the half's earlier MMAs done)
+    kABP = 15,       // +half: P in tensor memory
+    kABO = 17,       // +half: every MMA of the half done
+    kABDrain = 19,
+    kABVGo = 20,     // +stage: a masked tile's load has been issued
+    kANumBars = 22
+};
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+        "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+        "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+        "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+        : "memory");
+}
+
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const void* tmap, int x, int y, int z, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], "
+        "[%5];" ::"r"(dst),
+        "l"(tmap), "r"(x), "r"(y), "r"(z), "r"(bar)
+        : "memory");
+}
+
+// V as the B operand: [token][64 coordinates] rows of 128 bytes, 128-byte swizzle, the
+// coordinates (N) contiguous.  LBO: from one 64-coordinate block to the next; SBO: from
+// one 8-token group to the next.
+__device__ __forceinline__ uint32_t v_desc_lo(uint32_t addr) {
+    return ((addr >> 4) & 0x3FFFu) | ((kAHalf >> 4) << 16);
+}
+
+struct Args {
+    const int32_t* cu_q;      // [B + 1] first query row of each sequence
+    const int32_t* kv_lens;   // [B] tokens of each sequence (nullptr: its queries)
+    int B, total_q;
+    int max_kv;               // largest valid length (kv_lens)
+    int kv_pad;               // rows from one sequence's tokens to the next's (kv_lens)
+    const uint8_t* pages_ok;  // [B][kv_pad / 128] bit p: page p of the tile can be used (nullptr: all)
+    int Hq, heads, head0, G, QT;  // heads: kv heads of this launch, from head0 on; QT = 128 / G queries per half
+    float scale_log2;
+    const uint16_t* v;        // the values again, for the epilogue's repair
+    long long v_stride;       // elements from one token to the next
+    void* out;
+    int out_fp32;
+    uint32_t* err;
+};
+
+// Sequence of tile slot s: the last b with floor(cu[b] / q) + b <= s.  (Sequence b's
+// ceil(n_b / q) tiles fit its slots: floor((c + n) / q) + 1 >= floor(c / q) + ceil(n / q).)
+// All 32 lanes probe at once.
+__device__ __forceinline__ int find_seq(const int32_t* cu, int B, int q, int s, int lane) {
+    int lo = 0, n = B;  // the answer is in [lo, lo + n)
+    while (n > 1) {
+        const int step = (n + 31) / 32;
+        const int b = lo + lane * step;
+        const bool ok = lane * step < n && (lane == 0 || cu[b] / q + b <= s);
+        const int last = 31 - __clz(__ballot_sync(0xffffffffu, ok));
+        lo += last * step;
+        n = min(step, n - last * step);
+    }
+    return lo;
+}
+
+__global__ void __launch_bounds__(kAThreads, 1)
+    attend_tc_kernel(const __grid_constant__ CUtensorMap tq_map, const __grid_constant__ CUtensorMap tk_map,
+                     const __grid_constant__ CUtensorMap tv_map, const Args a) {
+    extern __shared__ __align__(1024) uint8_t smem[];
+    const uint32_t sbase = smem_u32(smem);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (sbase & 1023u) {
+        if (threadIdx.x == 0) atomicOr(a.err, TQ_DEVERR_INTERNAL);
+        return;
+    }
+    // ---- which rows
+    const int slot = (int)(blockIdx.x / (unsigned)a.heads), hk = (int)(blockIdx.x % (unsigned)a.heads);
+    const int QC = 2 * a.QT;
+    if (blockIdx.x == 0) {  // the whole list is looked through once
+        for (int b = threadIdx.x; b < a.B; b += kAThreads)
+            if (a.cu_q[b] < 0 || a.cu_q[b + 1] < a.cu_q[b] || a.cu_q[b + 1] > a.total_q)
+                atomicOr(a.err, TQ_DEVERR_SEQLEN);
+    }
+    const int b = find_seq(a.cu_q, a.B, QC, slot, lane);
+    const int c0 = a.cu_q[b], nq = a.cu_q[b + 1] - c0;
+    if (c0 < 0 || nq <= 0 || c0 + nq > a.total_q) return;
+    const int tiles = (nq + QC - 1) / QC;
+    const int rank = slot - (c0 / QC + b);
+    if (rank < 0 || rank >= tiles) return;
+    const int q0 = (tiles - 1 - rank) * QC;  // this CTA's first query; the sequence's heaviest tile first
+    const int kv_len = a.kv_lens ? a.kv_lens[b] : nq;
+    const int off = kv_len - nq;
+    if (off < 0 || (a.kv_lens && kv_len > a.max_kv)) {  // a length that cannot be: zero rows
+        if (threadIdx.x == 0) atomicOr(a.err, TQ_DEVERR_SEQLEN);
+        const int rows = min(QC, nq - q0) * a.G;
+        for (int i = threadIdx.x; i < rows * kDim; i += kAThreads) {
+            const int r = i / kDim;
+            const size_t o = ((size_t)(c0 + q0 + r / a.G) * a.Hq + (a.head0 + hk) * a.G + r % a.G) * kDim + i % kDim;
+            if (a.out_fp32) static_cast<float*>(a.out)[o] = 0.f;
+            else static_cast<__half*>(a.out)[o] = __ushort_as_half(0);
+        }
+        return;
+    }
+    const int kv_row = a.kv_lens ? b * a.kv_pad : c0;  // row of the sequence's token 0
+    // tiles of each half: up to its last query's position
+    auto tiles_of = [&](int h) {
+        const int first = q0 + h * a.QT;
+        return first < nq ? (off + min(nq, first + a.QT) + kAN - 1) / kAN : 0;
+    };
+    const int n0 = tiles_of(0), n1 = tiles_of(1), n = max(n0, n1);
+    const int masked_from = (off + q0 + 1) / kAN;  // first tile with a masked (row, token) pair
+
+    const uint32_t bars = sbase + kAOffBar;
+    auto bar = [&](int i) -> uint32_t { return bars + 8u * (uint32_t)i; };
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kAOffBar + 8 * kANumBars);
+    volatile int* abort = reinterpret_cast<volatile int*>(smem + kAOffBar + 8 * kANumBars + 4);
+    volatile int* repaired = reinterpret_cast<volatile int*>(smem + kAOffBar + 8 * kANumBars + 8);
+    auto give_up = [&] {
+        *abort = 1;
+        atomicOr(a.err, TQ_DEVERR_TIMEOUT);
+    };
+    if (threadIdx.x == 0) {
+        mbar_init(bar(kABQ), 1);
+        for (int s = 0; s < kAKStages; ++s) {
+            mbar_init(bar(kABKFull + s), 1);
+            mbar_init(bar(kABKEmpty + s), 1);
+        }
+        for (int s = 0; s < kAVStages; ++s) {
+            mbar_init(bar(kABVFull + s), 1);
+            mbar_init(bar(kABVEmpty + s), 1);
+            mbar_init(bar(kABVClean + s), 2);
+            mbar_init(bar(kABVGo + s), 1);
+        }
+        for (int h = 0; h < 2; ++h) {
+            mbar_init(bar(kABS + h), 1);
+            mbar_init(bar(kABP + h), 4);
+            mbar_init(bar(kABO + h), 1);
+        }
+        mbar_init(bar(kABDrain), 1);
+        *abort = 0;
+        *repaired = 0;
+        fence_mbar_init();
+    }
+    if (warp == 8) {
+        tmem_alloc(smem_u32(tmem_slot), 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    // columns: S0 (P0 over it) | S1 (P1) | O0 | O1
+
+    if (warp == 9) {
+        // ------------------------------------------------------------ producer
+        if (lane == 0) {
+            int kj = 0, vj = 0;
+            const int half_bytes = a.G * a.QT * 128;
+            mbar_arrive_expect_tx(bar(kABQ), (uint32_t)(half_bytes * 4));
+            for (int h = 0; h < 2; ++h)
+                for (int x = 0; x < 2; ++x)
+                    tma_load_3d(sbase + kAOffQ + h * kATile + x * kAHalf, &tq_map, 64 * x, (a.head0 + hk) * a.G,
+                                c0 + q0 + h * a.QT, bar(kABQ));
+            auto load = [&](const void* map, int full, int empty, uint32_t at, int stages, int j) -> bool {
+                const int s = j % stages;
+                if (!mbar_wait(bar(empty + s), (uint32_t)(j / stages & 1) ^ 1u, abort, kAWaitNs)) {
+                    give_up();
+                    return false;
+                }
+                mbar_arrive_expect_tx(bar(full + s), kATile);
+                for (int x = 0; x < 2; ++x)
+                    tma_load_3d(sbase + at + s * kATile + x * kAHalf, map, 64 * x, hk, kv_row + j * kAN, bar(full + s));
+                return true;
+            };
+            bool ok = load(&tk_map, kABKFull, kABKEmpty, kAOffK, kAKStages, 0);
+            kj = ok;
+            for (int j = 0; ok && j < n; ++j) {
+                if (j + 1 < n) {
+                    ok = load(&tk_map, kABKFull, kABKEmpty, kAOffK, kAKStages, j + 1);
+                    kj += ok;
+                }
+                if (ok) {
+                    ok = load(&tv_map, kABVFull, kABVEmpty, kAOffV, kAVStages, j);
+                    vj += ok;
+                    if (ok && j >= masked_from) mbar_arrive(bar(kABVGo + j % kAVStages));
+                }
+            }
+            // every copy lands before the CTA can exit
+            const volatile int never = 0;
+            mbar_wait(bar(kABQ), 0, &never, kAWaitNs);
+            for (int j = max(0, kj - kAKStages); j < kj; ++j)
+                mbar_wait(bar(kABKFull + j % kAKStages), (uint32_t)(j / kAKStages) & 1u, &never, kAWaitNs);
+            for (int j = max(0, vj - kAVStages); j < vj; ++j)
+                mbar_wait(bar(kABVFull + j % kAVStages), (uint32_t)(j / kAVStages) & 1u, &never, kAWaitNs);
+        }
+        __syncwarp();
+    } else if (warp == 8) {
+        // ------------------------------------------------------------ MMA issuer
+        if (lane == 0) {
+            const uint32_t id_s = idesc_f16(128, kAN), id_o = idesc_f16(128, kDim) | (1u << 16);
+            auto wait = [&](int i, int phase) -> bool {
+                if (mbar_wait(bar(i), (uint32_t)phase & 1u, abort, kAWaitNs)) return true;
+                give_up();
+                return false;
+            };
+            auto scores = [&](int h, int j) {
+                const uint32_t qa = sw128_desc_lo(sbase + kAOffQ + h * kATile);
+                const uint32_t kb = sw128_desc_lo(sbase + kAOffK + (j % kAKStages) * kATile);
+#pragma unroll
+                for (int ks = 0; ks < 8; ++ks) {
+                    const uint32_t o = (uint32_t)(ks & 3) * 2 + (uint32_t)(ks >> 2) * (kAHalf >> 4);
+                    umma_ss(tmem + h * 128, sw128_desc(qa + o), sw128_desc(kb + o), id_s, ks > 0);
+                }
+                umma_commit(bar(kABS + h));
+            };
+            auto values = [&](int h, int j) {
+                const uint32_t vb = v_desc_lo(sbase + kAOffV + (j % kAVStages) * kATile);
+#pragma unroll
+                for (int ks = 0; ks < 8; ++ks)
+                    umma_ts(tmem + 256 + h * 128, tmem + h * 128 + ks * 8, sw128_desc(vb + ks * (2048 >> 4)), id_o,
+                            (j | ks) > 0);
+            };
+            bool ok = wait(kABQ, 0) && wait(kABKFull, 0);
+            if (ok) {
+                tc_fence_after();
+                if (n0) scores(0, 0);
+                if (n1) scores(1, 0);
+                umma_commit(bar(kABKEmpty));
+            }
+            for (int j = 0; ok && j < n; ++j) {
+                const int vs = j % kAVStages;
+                ok = j >= masked_from ? wait(kABVClean + vs, (j - masked_from) / kAVStages) : wait(kABVFull + vs, j / kAVStages);
+                if (ok && j + 1 < n) ok = wait(kABKFull + (j + 1) % kAKStages, (j + 1) / kAKStages);
+                for (int h = 0; ok && h < 2; ++h) {
+                    const int nh = h ? n1 : n0;
+                    if (j >= nh) continue;
+                    ok = wait(kABP + h, j);
+                    if (!ok) break;
+                    tc_fence_after();
+                    values(h, j);
+                    if (j + 1 < nh) scores(h, j + 1);
+                    else umma_commit(bar(kABO + h));
+                }
+                if (ok) {
+                    umma_commit(bar(kABVEmpty + vs));
+                    if (j + 1 < n) umma_commit(bar(kABKEmpty + (j + 1) % kAKStages));
+                }
+            }
+            // nothing is in flight when the CTA exits
+            umma_commit(bar(kABDrain));
+            const volatile int never = 0;
+            mbar_wait(bar(kABDrain), 0, &never, kAWaitNs);
+        }
+        __syncwarp();
+    } else if (warp >= 10) {
+        // ------------------------------------------------------------ masked tiles' values
+        for (int j = masked_from; j < n; ++j) {
+            const int s = j % kAVStages;
+            // (these warps do not follow the unmasked tiles' phases of the stage: its load's
+            // issue tells them that the phase of this tile is the current one)
+            if (!mbar_wait_warp(bar(kABVGo + s), (uint32_t)((j - masked_from) / kAVStages) & 1u, abort, kAWaitNs) ||
+                !mbar_wait_warp(bar(kABVFull + s), (uint32_t)(j / kAVStages) & 1u, abort, kAWaitNs)) {
+                give_up();
+                break;
+            }
+            uint4* v = reinterpret_cast<uint4*>(smem + kAOffV + s * kATile);
+            bool any = false;
+#pragma unroll 4
+            for (int i = threadIdx.x - 320; i < (int)(kATile / 16); i += 64) {
+                uint4 x = v[i];
+                uint32_t w[4] = {x.x, x.y, x.z, x.w};
+                bool bad = false;
+#pragma unroll
+                for (int p = 0; p < 4; ++p) {
+                    // bit 15 / 31: the half's exponent is all ones
+                    const uint32_t e = ((w[p] & 0x7C007C00u) + 0x04000400u) & 0x80008000u;
+                    if (e) {
+                        bad = true;
+                        if (e & 0x8000u) w[p] &= 0xFFFF0000u;
+                        if (e & 0x80000000u) w[p] &= 0x0000FFFFu;
+                    }
+                }
+                if (bad) {
+                    any = true;
+                    v[i] = make_uint4(w[0], w[1], w[2], w[3]);
+                }
+            }
+            if (any) *repaired = 1;
+            fence_proxy_async_shared();
+            mbar_arrive_warp(bar(kABVClean + s));
+        }
+    } else {
+        // ------------------------------------------------------------ softmax
+        const int h = warp >> 2, row = threadIdx.x & 127;
+        const int nh = h ? n1 : n0;
+        const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // this warp's 32 lanes
+        const uint32_t ts = tmem + h * 128 + lanes, to = tmem + 256 + h * 128 + lanes;
+        const int qi = q0 + h * a.QT + row / a.G;           // this row's query
+        const bool live = row < a.G * a.QT && qi < nq;
+        const int limit = live ? off + qi : -1;             // its last token
+        const int half_masked = (off + q0 + h * a.QT + 1) / kAN;
+        float m = -INFINITY, l = 0.f;
+        bool ok = true;
+        for (int j = 0; j < nh; ++j) {
+            if (!mbar_wait_warp(bar(kABS + h), (uint32_t)j & 1u, abort, kAWaitNs)) {
+                give_up();
+                ok = false;
+                break;
+            }
+            tc_fence_after();
+            uint32_t s[4][32];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) tmem_ld32(ts + 32 * q, s[q]);
+            tmem_ld_wait();
+            const int okp = a.pages_ok ? a.pages_ok[(size_t)b * (a.kv_pad / kAN) + j] : 0xff;
+            if (j >= half_masked || okp != 0xff) {
+                const int lim = limit - j * kAN;
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        if (32 * q + i > lim || !((okp >> (2 * q + i / 16)) & 1)) s[q][i] = 0xFF800000u;  // -inf
+            }
+            float mx[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                mx[q] = __uint_as_float(s[q][0]);
+#pragma unroll
+                for (int i = 1; i < 32; ++i) mx[q] = fmaxf(mx[q], __uint_as_float(s[q][i]));
+            }
+            const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.scale_log2;
+            const bool grow = top > m + kRescale || (m == -INFINITY && top > m);
+            if (__any_sync(0xffffffffu, grow)) {
+                const float mn = grow ? top : m;
+                if (j > 0) {
+                    const float f = grow ? ex2(m - mn) : 1.f;  // (first maximum: ex2(-inf) = 0)
+                    l *= f;
+#pragma unroll
+                    for (int q = 0; q < 8; ++q) {
+                        uint32_t o[16];
+                        tmem_ld16(to + 16 * q, o);
+                        tmem_ld_wait();
+                        uint32_t lo[8], hi[8];
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            lo[i] = __float_as_uint(__uint_as_float(o[i]) * f);
+                            hi[i] = __float_as_uint(__uint_as_float(o[8 + i]) * f);
+                        }
+                        tmem_st8(to + 16 * q, lo);
+                        tmem_st8(to + 16 * q + 8, hi);
+                    }
+                }
+                m = mn;
+            }
+            const float mm = m == -INFINITY ? 0.f : m;
+            float2 sum[2] = {{0.f, 0.f}, {0.f, 0.f}};
+            const float2 sc = make_float2(a.scale_log2, a.scale_log2), nm = make_float2(-mm, -mm);
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+                uint32_t p[32];
+#pragma unroll
+                for (int i = 0; i < 32; ++i) {
+                    const int e = 64 * q + 2 * i;
+                    float2 x = make_float2(__uint_as_float(s[e / 32][e % 32]), __uint_as_float(s[e / 32][e % 32 + 1]));
+                    x = __ffma2_rn(x, sc, nm);
+                    x.x = ex2(x.x);
+                    x.y = ex2(x.y);
+                    sum[i & 1] = __fadd2_rn(sum[i & 1], x);
+                    const __half2 hp = __floats2half2_rn(x.x, x.y);
+                    p[i] = *reinterpret_cast<const uint32_t*>(&hp);
+                }
+                tmem_st32(ts + 32 * q, p);
+            }
+            l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+            tmem_st_wait();
+            tc_fence_before();
+            mbar_arrive_warp(bar(kABP + h));
+        }
+        if (ok && nh > 0) {
+            if (!mbar_wait_warp(bar(kABO + h), 0, abort, kAWaitNs)) {
+                give_up();
+                ok = false;
+            }
+        }
+        if (ok && nh > 0) {
+            tc_fence_after();
+            const float inv = l != 0.f ? 1.f / l : 0.f;  // (no token: a zero row)
+            const size_t orow = ((size_t)(c0 + qi) * a.Hq + (a.head0 + hk) * a.G + row % a.G) * kDim;
+            const bool fix = *repaired != 0;
+#pragma unroll 1
+            for (int q = 0; q < 4; ++q) {
+                uint32_t o[32];
+                tmem_ld32(to + 32 * q, o);
+                tmem_ld_wait();
+                if (!live) continue;
+                float f[32];
+#pragma unroll
+                for (int i = 0; i < 32; ++i) f[i] = __uint_as_float(o[i]) * inv;
+                if (fix) {
+                    for (int t = masked_from * kAN; t <= limit; ++t) {
+                        const __half* v = reinterpret_cast<const __half*>(a.v) + (kv_row + t) * a.v_stride + hk * kDim + 32 * q;
+#pragma unroll
+                        for (int i = 0; i < 32; ++i) {
+                            const float x = __half2float(v[i]);
+                            if (!isfinite(x)) f[i] += x;
+                        }
+                    }
+                }
+                if (a.out_fp32) {
+                    float4* d = reinterpret_cast<float4*>(static_cast<float*>(a.out) + orow + 32 * q);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) d[i] = make_float4(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]);
+                } else {
+                    uint4* d = reinterpret_cast<uint4*>(static_cast<__half*>(a.out) + orow + 32 * q);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        uint32_t w[4];
+#pragma unroll
+                        for (int p = 0; p < 4; ++p) {
+                            const __half2 x = __floats2half2_rn(f[8 * i + 2 * p], f[8 * i + 2 * p + 1]);
+                            w[p] = *reinterpret_cast<const uint32_t*>(&x);
+                        }
+                        d[i] = make_uint4(w[0], w[1], w[2], w[3]);
+                    }
+                }
+            }
+            tc_fence_before();
+        }
+    }
+    __syncthreads();
+    if (warp == 8) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_attend(const tq_ctx* ctx, const AttendCall& c, cudaStream_t stream) {
+    Args a{};
+    a.cu_q = c.cu_q;
+    a.kv_lens = c.kv_lens;
+    a.B = c.B;
+    a.total_q = c.total_q;
+    a.max_kv = c.max_kv;
+    a.kv_pad = c.kv_pad;
+    a.pages_ok = c.pages_ok;
+    a.Hq = c.Hq;
+    a.heads = c.heads;
+    a.head0 = c.head0;
+    a.G = c.G;
+    a.QT = 128 / c.G;
+    a.scale_log2 = c.scale * 1.4426950408889634f;
+    a.v = c.v;
+    a.v_stride = c.v_stride;
+    a.out = c.out;
+    a.out_fp32 = c.out_fp32;
+    a.err = ctx->dev_error;
+    const long long kv_rows = c.kv_lens ? (long long)c.B * c.kv_pad : c.total_q;
+    CUtensorMap mq, mk, mv;
+    if (!encode_heads_tmap(&mq, c.q, c.Hq, c.total_q, c.q_stride, c.G, a.QT) ||
+        !encode_heads_tmap(&mk, c.k, c.heads, kv_rows, c.k_stride, 1, kAN) ||
+        !encode_heads_tmap(&mv, c.v, c.heads, kv_rows, c.v_stride, 1, kAN))
+        return cudaErrorInvalidValue;
+    cudaError_t e = cudaFuncSetAttribute(attend_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kASmem);
+    if (e != cudaSuccess) return e;
+    // slots of all sequences: floor(total / q) + B bounds every sequence's last one
+    const long long slots = (long long)c.total_q / (2 * a.QT) + c.B;
+    if (slots * c.heads > 0x7FFFFFFFll) return cudaErrorInvalidValue;
+    attend_tc_kernel<<<(unsigned)(slots * c.heads), kAThreads, kASmem, stream>>>(mq, mk, mv, a);
+    e = cudaGetLastError();
+    if (e == cudaSuccess) count_launches(1);
+    return e;
+}
+
+}  // namespace tq

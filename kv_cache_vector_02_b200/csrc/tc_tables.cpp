@@ -172,7 +172,8 @@ PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
 std::once_flag g_encode_once;
 }  // namespace
 
-bool encode_rows_tmap(CUtensorMap* map, const void* x, int rows) {
+namespace {
+bool find_encode() {
     std::call_once(g_encode_once, [] {
         void* fn = nullptr;
         cudaDriverEntryPointQueryResult q;
@@ -181,12 +182,30 @@ bool encode_rows_tmap(CUtensorMap* map, const void* x, int rows) {
             g_encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
         cudaGetLastError();
     });
-    if (!g_encode || rows < 1) return false;
+    return g_encode != nullptr;
+}
+}  // namespace
+
+bool encode_rows_tmap(CUtensorMap* map, const void* x, int rows) {
+    if (!find_encode() || rows < 1) return false;
     cuuint64_t dims[2] = {cuuint64_t(kD), cuuint64_t(rows)};
     cuuint64_t strides[1] = {cuuint64_t(kD) * 2};
     cuuint32_t box[2] = {64, 128};
     cuuint32_t estr[2] = {1, 1};
     const CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, const_cast<void*>(x), dims, strides, box,
+                                estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS;
+}
+
+bool encode_heads_tmap(CUtensorMap* map, const void* x, int heads, long long rows, long long stride, int box_heads,
+                       int box_rows) {
+    if (!find_encode() || rows < 1 || heads < 1) return false;
+    cuuint64_t dims[3] = {cuuint64_t(kD), cuuint64_t(heads), cuuint64_t(rows)};
+    cuuint64_t strides[2] = {cuuint64_t(kD) * 2, cuuint64_t(stride) * 2};
+    cuuint32_t box[3] = {64, cuuint32_t(box_heads), cuuint32_t(box_rows)};
+    cuuint32_t estr[3] = {1, 1, 1};
+    const CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<void*>(x), dims, strides, box,
                                 estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                                 CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS;

@@ -76,6 +76,47 @@ struct NvtxRange {
     NvtxRange& operator=(const NvtxRange&) = delete;
 };
 
+// Makes ctx's device the current one for the length of a call.
+struct DeviceGuard {
+    int before = -1;
+    bool ok;
+    explicit DeviceGuard(int device) {
+        ok = cudaGetDevice(&before) == cudaSuccess && (before == device || cudaSetDevice(device) == cudaSuccess);
+        if (before == device) before = -1;
+    }
+    ~DeviceGuard() {
+        if (before >= 0) cudaSetDevice(before);
+    }
+    DeviceGuard(const DeviceGuard&) = delete;
+    DeviceGuard& operator=(const DeviceGuard&) = delete;
+};
+
+// Rows of `width` bytes, `stride` bytes apart.
+struct Rows {
+    const void* p;
+    long long n, width, stride;
+    uintptr_t at() const { return reinterpret_cast<uintptr_t>(p); }
+    uintptr_t end() const { return at() + uintptr_t((n - 1) * stride + width); }
+};
+
+// Whether a and b share a byte, except that rows of the same stride may lie between one
+// another (columns of one matrix).
+bool overlap(const Rows& a, const Rows& b) {
+    if (!a.p || !b.p || a.n < 1 || b.n < 1 || a.end() <= b.at() || b.end() <= a.at()) return false;
+    if (a.stride != b.stride) return true;
+    const Rows& lo = a.at() <= b.at() ? a : b;
+    const Rows& hi = a.at() <= b.at() ? b : a;
+    const long long d = (long long)((hi.at() - lo.at()) % uintptr_t(lo.stride));
+    return d < lo.width || d + hi.width > lo.stride;
+}
+
+Rows fp16_rows(const void* p, int T, int H, int64_t stride) { return Rows{p, T, (long long)H * kDim * 2, stride * 2}; }
+
+// A token stride that a row of H heads fits: a multiple of 16 bytes, below 2^40 bytes.
+bool good_stride(int64_t stride, int H) {
+    return stride % 8 == 0 && stride >= (int64_t)H * kDim && stride < (int64_t(1) << 39);
+}
+
 // Records that ctx's parameters are in use by work queued on `stream` up to now.
 // Returns false if the event could not be created or recorded.
 bool note_use(const tq_ctx* ctx, cudaStream_t stream) {
@@ -394,6 +435,110 @@ tq_status tq_prefill_attention(const tq_ctx* ctx, const uint16_t* q, const uint8
     if (tq::launch_prefill(ctx, q, k_cache, v_cache, num_blocks, block_table, max_blocks, q_start, Tq, Hq, Hkv, scale,
                            out, out_fp32, s) != cudaSuccess)
         return TQ_ERR_CUDA;
+    return note_use(ctx, s) ? TQ_OK : TQ_ERR_CUDA;
+}
+
+tq_status tq_rope_plan(int rot_dim, int layout, double base, int scaling, double factor, double original_len,
+                       double low, double high, tq_rope_table* out) {
+    if (!out) return TQ_ERR_INVALID_ARG;
+    std::memset(out, 0, sizeof(*out));
+    if (layout != TQ_ROPE_HALF && layout != TQ_ROPE_INTERLEAVED) return TQ_ERR_UNSUPPORTED;
+    if (scaling < TQ_ROPE_SCALE_NONE || scaling > TQ_ROPE_SCALE_YARN) return TQ_ERR_UNSUPPORTED;
+    if (rot_dim < 2 || rot_dim > kDim || rot_dim % 2 != 0) return TQ_ERR_INVALID_ARG;
+    if (!(base > 1.0) || !std::isfinite(base)) return TQ_ERR_INVALID_ARG;
+    if (scaling != TQ_ROPE_SCALE_NONE && (!(factor >= 1.0) || !std::isfinite(factor))) return TQ_ERR_INVALID_ARG;
+    if (scaling == TQ_ROPE_SCALE_NTK && rot_dim <= 2) return TQ_ERR_INVALID_ARG;
+    if (scaling == TQ_ROPE_SCALE_BANDS || scaling == TQ_ROPE_SCALE_YARN) {
+        if (!(original_len > 0.0) || !(low > 0.0) || !(high > low)) return TQ_ERR_INVALID_ARG;
+        if (!std::isfinite(original_len) || !std::isfinite(high)) return TQ_ERR_INVALID_ARG;
+    }
+    tq::fill_rope_table(rot_dim, layout, base, scaling, factor, original_len, low, high, out);
+    return TQ_OK;
+}
+
+tq_status tq_rope(const tq_rope_table* table, const uint16_t* q, int64_t q_stride, const uint16_t* k,
+                  int64_t k_stride, int T, int Hq, int Hkv, const int32_t* positions, uint16_t* q_out,
+                  int64_t q_out_stride, uint16_t* k_out, int64_t k_out_stride, int transpose, void* stream) {
+    NvtxRange nvtx("tq_rope");
+    if (!table || T < 0) return TQ_ERR_INVALID_ARG;
+    if (table->rot_dim < 2 || table->rot_dim > kDim || table->rot_dim % 2 != 0) return TQ_ERR_INVALID_ARG;
+    if (table->layout != TQ_ROPE_HALF && table->layout != TQ_ROPE_INTERLEAVED) return TQ_ERR_INVALID_ARG;
+    if (T == 0) return TQ_OK;
+    if (!q && !k) return TQ_ERR_INVALID_ARG;
+    if (!q) Hq = 0;
+    if (!k) Hkv = 0;
+    if ((q && Hq < 1) || (k && Hkv < 1) || Hq > 65536 || Hkv > 65536) return TQ_ERR_INVALID_ARG;
+    if (!positions || (q && !q_out) || (k && !k_out)) return TQ_ERR_INVALID_ARG;
+    if ((q && (!good_stride(q_stride, Hq) || !good_stride(q_out_stride, Hq))) ||
+        (k && (!good_stride(k_stride, Hkv) || !good_stride(k_out_stride, Hkv))))
+        return TQ_ERR_INVALID_ARG;
+    if (!aligned16(q) || !aligned16(k) || (q && !aligned16(q_out)) || (k && !aligned16(k_out)))
+        return TQ_ERR_INVALID_ARG;
+    const Rows qi = fp16_rows(q, T, Hq, q_stride), ki = fp16_rows(k, T, Hkv, k_stride);
+    const Rows qo = fp16_rows(q ? q_out : nullptr, T, Hq, q_out_stride);
+    const Rows ko = fp16_rows(k ? k_out : nullptr, T, Hkv, k_out_stride);
+    const Rows ps{positions, 1, (long long)T * 4, (long long)T * 4};
+    const bool q_place = q && q == q_out && q_stride == q_out_stride;
+    const bool k_place = k && k == k_out && k_stride == k_out_stride;
+    if ((!q_place && overlap(qi, qo)) || (!k_place && overlap(ki, ko)) || overlap(qo, ki) || overlap(ko, qi) ||
+        overlap(qo, ko) || overlap(qo, ps) || overlap(ko, ps))
+        return TQ_ERR_INVALID_ARG;
+    tq::RopeCall c{};
+    c.table = table;
+    c.q = q;
+    c.k = k;
+    c.q_out = q_out;
+    c.k_out = k_out;
+    c.q_stride = q_stride;
+    c.k_stride = k_stride;
+    c.q_out_stride = q_out_stride;
+    c.k_out_stride = k_out_stride;
+    c.T = T;
+    c.Hq = Hq;
+    c.Hkv = Hkv;
+    c.positions = positions;
+    c.transpose = transpose;
+    return tq::launch_rope(c, static_cast<cudaStream_t>(stream)) == cudaSuccess ? TQ_OK : TQ_ERR_CUDA;
+}
+
+tq_status tq_prompt_attention(const tq_ctx* ctx, const uint16_t* q, int64_t q_stride, const uint16_t* k,
+                              int64_t k_stride, const uint16_t* v, int64_t v_stride, int T, const int32_t* cu_seqlens,
+                              int B, int Hq, int Hkv, float scale, void* out, int out_fp32, void* stream) {
+    NvtxRange nvtx("tq_prompt_attention");
+    if (!ctx || ctx->host_only || T < 0 || B < 0 || Hq < 1 || Hkv < 1) return TQ_ERR_INVALID_ARG;
+    if (Hq % Hkv != 0 || Hq / Hkv > 128) return TQ_ERR_INVALID_ARG;
+    if (!(scale >= 0.f) || !std::isfinite(scale)) return TQ_ERR_INVALID_ARG;
+    if (T == 0 || B == 0) return TQ_OK;
+    if (!q || !k || !v || !cu_seqlens || !out) return TQ_ERR_INVALID_ARG;
+    if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(out)) return TQ_ERR_INVALID_ARG;
+    if (!good_stride(q_stride, Hq) || !good_stride(k_stride, Hkv) || !good_stride(v_stride, Hkv))
+        return TQ_ERR_INVALID_ARG;
+    const long long out_bytes = (long long)T * Hq * kDim * (out_fp32 ? 4 : 2);
+    const Rows o{out, 1, out_bytes, out_bytes};
+    if (overlap(o, fp16_rows(q, T, Hq, q_stride)) || overlap(o, fp16_rows(k, T, Hkv, k_stride)) ||
+        overlap(o, fp16_rows(v, T, Hkv, v_stride)))
+        return TQ_ERR_INVALID_ARG;
+    if (scale == 0.f) scale = 1.0f / std::sqrt(float(kDim));
+    DeviceGuard dev(ctx->device);
+    if (!dev.ok) return TQ_ERR_CUDA;
+    tq::AttendCall c{};
+    c.q = q;
+    c.k = k;
+    c.v = v;
+    c.q_stride = q_stride;
+    c.k_stride = k_stride;
+    c.v_stride = v_stride;
+    c.cu_q = cu_seqlens;
+    c.B = B;
+    c.total_q = T;
+    c.Hq = Hq;
+    c.heads = Hkv;
+    c.G = Hq / Hkv;
+    c.scale = scale;
+    c.out = out;
+    c.out_fp32 = out_fp32;
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (tq::launch_attend(ctx, c, s) != cudaSuccess) return TQ_ERR_CUDA;
     return note_use(ctx, s) ? TQ_OK : TQ_ERR_CUDA;
 }
 

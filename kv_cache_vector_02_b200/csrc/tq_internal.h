@@ -138,6 +138,37 @@ constexpr int kDecodeTailMax = 256;
 cudaError_t launch_prefill(const tq_ctx* ctx, const uint16_t* q, const uint8_t* kc, const uint8_t* vc, int num_blocks,
                            const int32_t* block_table, int max_blocks, int q_start, int Tq, int Hq, int Hkv, float scale,
                            void* out, int out_fp32, cudaStream_t stream);
+// Rotary positions (rope.cu); q or k null: not there.
+struct RopeCall {
+    const tq_rope_table* table;
+    const uint16_t* q;
+    const uint16_t* k;
+    uint16_t* q_out;
+    uint16_t* k_out;
+    long long q_stride, k_stride, q_out_stride, k_out_stride;  // elements from a token to the next
+    int T, Hq, Hkv;
+    const int32_t* positions;
+    int transpose;
+};
+void fill_rope_table(int rot_dim, int layout, double base, int scaling, double factor, double original_len, double low,
+                     double high, tq_rope_table* out);
+cudaError_t launch_rope(const RopeCall& c, cudaStream_t stream);
+// Causal attention of ragged sequences over fp16 keys and values (attend_tc.cu).
+struct AttendCall {
+    const uint16_t* q;       // [total_q] rows of Hq heads, q_stride elements apart
+    const uint16_t* k;       // rows of `heads` kv heads; row cu_q[b] + t, or (kv_lens) b * kv_pad + t
+    const uint16_t* v;
+    long long q_stride, k_stride, v_stride;
+    const int32_t* cu_q;     // [B + 1]
+    const int32_t* kv_lens;  // [B], or null: a sequence's tokens are its queries
+    int B, total_q, max_kv, kv_pad;
+    const uint8_t* pages_ok; // [B][kv_pad / 128], a bit per page, or null
+    int Hq, heads, head0, G;
+    float scale;
+    void* out;
+    int out_fp32;
+};
+cudaError_t launch_attend(const tq_ctx* ctx, const AttendCall& c, cudaStream_t stream);
 cudaError_t launch_decode(const tq_ctx* ctx, const DecodePlan& plan, const uint16_t* q, const uint8_t* kc,
                           const uint8_t* vc, int num_blocks, const int32_t* block_table, int max_blocks,
                           const int32_t* seq_lens, int B, int Hq, int Hkv, int max_seq_len, const DecodeTail& tail,

@@ -24,12 +24,20 @@ KIND_KEY, KIND_VALUE = 0, 1
 DEVERR_SLOT, DEVERR_BLOCK, DEVERR_SEQLEN, DEVERR_TIMEOUT = 0x1, 0x2, 0x4, 0x8
 
 FLAG_SPHERE_CODEBOOK, FLAG_HOST_ONLY = 0x1, 0x4
+ROPE_HALF, ROPE_INTERLEAVED = 0, 1
+ROPE_SCALE_NONE, ROPE_SCALE_LINEAR, ROPE_SCALE_NTK, ROPE_SCALE_BANDS, ROPE_SCALE_YARN = range(5)
 
 EXPORTED = ("tq_init", "tq_init_ex", "tq_init_host", "tq_destroy", "tq_chunk_bytes", "tq_code_bits", "tq_export_params", "tq_compress",
             "tq_decompress", "tq_decode_workspace_bytes", "tq_decode_attention", "tq_decode_attention_window",
-            "tq_prefill_attention",
+            "tq_prefill_attention", "tq_rope_plan", "tq_rope", "tq_prompt_attention",
             "tq_decode_attention_noalloc",
             "tq_get_device_error", "tq_debug_stall", "tq_launch_count", "tq_status_string")
+
+
+class RopeTable(ctypes.Structure):
+    """tq_rope_table: the frequencies of a rotary embedding (see tq_rope_plan)."""
+    _fields_ = [("rot_dim", ctypes.c_int32), ("layout", ctypes.c_int32), ("mscale", ctypes.c_float),
+                ("reserved", ctypes.c_int32), ("turns", ctypes.c_uint64 * 64)]
 
 
 class TQError(RuntimeError):
@@ -43,6 +51,7 @@ def _load():
         raise ImportError("libtq.so not built: run `python -m kv_cache_vector_02_b200.build`")
     L = ctypes.CDLL(str(_LIB_PATH))
     P, I, Z, U64, F = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.c_uint64, ctypes.c_float
+    I64, D = ctypes.c_int64, ctypes.c_double
     sig = {
         "tq_init": (I, [I, I, U64, I, I, ctypes.POINTER(P)]),
         "tq_init_host": (I, [I, I, U64, I, I, ctypes.POINTER(P)]),
@@ -57,6 +66,9 @@ def _load():
         "tq_decode_attention": (I, [P, P, P, P, I, P, I, P, I, I, I, I, F, P, I, P, Z, P]),
         "tq_decode_attention_window": (I, [P, P, P, P, I, P, I, P, I, I, I, I, P, P, P, I, F, P, I, P, Z, P]),
         "tq_prefill_attention": (I, [P, P, P, P, I, P, I, I, I, I, I, F, P, I, P]),
+        "tq_rope_plan": (I, [I, I, D, I, D, D, D, D, ctypes.POINTER(RopeTable)]),
+        "tq_rope": (I, [ctypes.POINTER(RopeTable), P, I64, P, I64, I, I, I, P, P, I64, P, I64, I, P]),
+        "tq_prompt_attention": (I, [P, P, I64, P, I64, P, I64, I, P, I, I, I, F, P, I, P]),
         "tq_decode_attention_noalloc": (I, [P, P, P, P, I, P, I, P, I, I, I, I, F, P, I, P]),
         "tq_get_device_error": (I, [P, P, ctypes.POINTER(ctypes.c_uint32)]),
         "tq_debug_stall": (I, [P, I]),
@@ -287,6 +299,104 @@ def tq_prefill_attention(ctx: Context, q, k_cache, v_cache, block_table, q_start
                                      _ptr(block_table), int(block_table.shape[0]), int(q_start), Tq, Hq, Hkv,
                                      float(scale), _ptr(out), 1 if out.dtype == torch.float32 else 0,
                                      _stream(stream)), what)
+
+
+def _token_stride(t, what: str, name: str) -> int:
+    """Elements from one token of a [T, H, 128] fp16 tensor to the next; its heads must lie
+    side by side (a view into a fused projection may have a longer stride)."""
+    import torch
+    T, H, d = t.shape if t.dim() == 3 else (0, 0, 0)
+    ok = t.dim() == 3 and d == 128 and t.dtype is torch.float16 and H > 0
+    if ok and T > 0:
+        st = t.stride()
+        ok = st[2] == 1 and (H == 1 or st[1] == 128) and (T == 1 or (st[0] >= 128 * H and st[0] % 8 == 0))
+    if not ok:
+        raise TQError(TQ_ERR_INVALID_ARG, "%s: %s must be [T, H, 128] of %s, each token's heads contiguous, got %s %s "
+                      "with strides %s" % (what, name, torch.float16, tuple(t.shape), t.dtype, tuple(t.stride())))
+    return t.stride(0) if T > 1 else 128 * H
+
+
+def _same_device(what: str, first, *others):
+    """Every tensor on one device; the stream of that device's current stream by default."""
+    for t in others:
+        if t is not None and t.device != first.device:
+            raise TQError(TQ_ERR_INVALID_ARG, "%s: tensors on %s and %s must be on one device" % (
+                what, first.device, t.device))
+
+
+def _stream_on(stream, t) -> int:
+    if stream is None and t.is_cuda:
+        import torch
+        return torch.cuda.current_stream(t.device).cuda_stream
+    return 0 if stream is None else _stream(stream)
+
+
+def tq_rope_plan(rot_dim: int = 128, layout: int = ROPE_HALF, base: float = 10000.0, scaling: int = ROPE_SCALE_NONE,
+                 factor: float = 1.0, original_len: float = 0.0, low: float = 0.0, high: float = 0.0) -> RopeTable:
+    """Frequencies of a rotary embedding (host; see tq.h for the scalings)."""
+    t = RopeTable()
+    _check(_lib.tq_rope_plan(rot_dim, layout, base, scaling, factor, original_len, low, high, ctypes.byref(t)),
+           "tq_rope_plan")
+    return t
+
+
+def tq_rope(table: RopeTable, q, k, positions, q_out=None, k_out=None, transpose: bool = False, stream=None):
+    """Rotary positions: q [T, Hq, 128], k [T, Hkv, 128] fp16 (either may be None; the token
+    stride may be longer than a row), positions [T] int32.  q_out, k_out default to q, k (in
+    place)."""
+    import torch
+    what = "tq_rope"
+    ref = q if q is not None else k
+    if ref is None:
+        raise TQError(TQ_ERR_INVALID_ARG, "tq_rope: no input")
+    T = int(ref.shape[0])
+    args, heads = [], []
+    for x, o, n in ((q, q_out, "q"), (k, k_out, "k")):
+        if x is None:
+            if o is not None:
+                raise TQError(TQ_ERR_INVALID_ARG, "%s: %s_out without %s" % (what, n, n))
+            args.append((None, 0, None, 0))
+            heads.append(0)
+            continue
+        o = x if o is None else o
+        sx, so = _token_stride(x, what, n), _token_stride(o, what, n + "_out")
+        if x.shape[0] != T or o.shape != x.shape:
+            raise TQError(TQ_ERR_INVALID_ARG, "%s: %s and its output must be of one shape, with as many tokens as the "
+                          "other input" % (what, n))
+        args.append((x, sx, o, so))
+        heads.append(int(x.shape[1]))
+    _expect(positions, (T,), (torch.int32,), what, "positions")
+    (q, sq, qo, sqo), (k, sk, ko, sko) = args
+    _same_device(what, ref, q, k, qo, ko, positions)
+    s = _stream_on(stream, ref)
+    call = (ctypes.byref(table), _ptr(q), sq, _ptr(k), sk, T, heads[0], heads[1], _ptr(positions), _ptr(qo), sqo,
+            _ptr(ko), sko, 1 if transpose else 0, s)
+    if ref.is_cuda and ref.device.index != torch.cuda.current_device():
+        with torch.cuda.device(ref.device):
+            _check(_lib.tq_rope(*call), what)
+    else:
+        _check(_lib.tq_rope(*call), what)
+
+
+def tq_prompt_attention(ctx: Context, q, k, v, cu_seqlens, out, scale: float = 0.0, stream=None):
+    """Causal attention over packed prompts: q [T, Hq, 128], k, v [T, Hkv, 128] fp16 (token
+    strides may be longer than a row), cu_seqlens [B + 1] int32, out [T, Hq, 128] fp16 or
+    fp32 (see tq.h)."""
+    import torch
+    what = "tq_prompt_attention"
+    sq, sk, sv = _token_stride(q, what, "q"), _token_stride(k, what, "k"), _token_stride(v, what, "v")
+    T, Hq, Hkv = int(q.shape[0]), int(q.shape[1]), int(k.shape[1])
+    if k.shape[0] != T or v.shape != k.shape:
+        raise TQError(TQ_ERR_INVALID_ARG, "%s: k and v must be of one shape, with q's tokens" % what)
+    _expect(cu_seqlens, (None,), (torch.int32,), what, "cu_seqlens")
+    B = int(cu_seqlens.shape[0]) - 1
+    if B < 0:
+        raise TQError(TQ_ERR_INVALID_ARG, "%s: cu_seqlens must have B + 1 entries" % what)
+    _expect(out, (T, Hq, 128), (torch.float16, torch.float32), what, "out")
+    _same_device(what, q, k, v, cu_seqlens, out)
+    _check(_lib.tq_prompt_attention(ctx.handle, _ptr(q), sq, _ptr(k), sk, _ptr(v), sv, T, _ptr(cu_seqlens), B, Hq, Hkv,
+                                    float(scale), _ptr(out), 1 if out.dtype == torch.float32 else 0,
+                                    _stream_on(stream, q)), what)
 
 
 NOALLOC_SCRATCH_BYTES = 8 << 20
