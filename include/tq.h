@@ -363,6 +363,45 @@ TQ_API tq_status tq_prompt_attention(const tq_ctx* ctx, const uint16_t* q_dev, i
                                      void* out_dev, int out_fp32, void* stream);
 
 /*
+ * tq_chunk_workspace_bytes -- device scratch needed by tq_chunk_attention for B sequences,
+ * total_q queries in all, Hq query heads over Hkv kv heads and at most max_seq_len cached
+ * tokens a sequence (0 on invalid arguments).  Any contents; nothing in it outlives a call.
+ * Two calls that run at the same time need separate workspaces.
+ */
+TQ_API size_t tq_chunk_workspace_bytes(const tq_ctx* ctx, int B, int total_q, int Hq, int Hkv, int max_seq_len);
+
+/*
+ * tq_chunk_attention -- causal attention of a ragged batch of chunks of new tokens over the
+ * paged compressed cache: pieces of prompts, drafted tokens to verify and single tokens in
+ * one call.  Sequence b has n_b = cu_q[b + 1] - cu_q[b] queries (rows cu_q[b] .. of q) and
+ * L_b = seq_lens[b] cached tokens, the chunk's own among them (compress the chunk first);
+ * its query i attends to the tokens 0 .. L_b - n_b + i:
+ *   s_t = scale * ( <q_i, k_hat_t> + gamma_t*sqrt(pi/2)/d * <S q_i, 2 sigma_t - 1> ),
+ *   o_i = sum_t softmax(s)_t * v_hat_t
+ * (tq_prefill_attention's sums, for many sequences; the decompressed keys and values are
+ * rounded to fp16).
+ *   q_dev          : [total_q][Hq][128] fp16, device, 16-byte aligned; Hq / Hkv 1 .. 128.
+ *   cu_q_dev       : [B + 1] int32, non-decreasing, 0 .. total_q; as tq_prompt_attention's
+ *                    cu_seqlens.  n_b = 0 is allowed.
+ *   block_table_dev: [B][max_blocks] int32.  A block id outside [0, num_blocks) skips the
+ *                    page and sets TQ_DEVERR_BLOCK.
+ *   seq_lens_dev   : [B] int32, n_b <= L_b <= max_seq_len and <= max_blocks*16 (else the
+ *                    sequence's outputs are zeroed and TQ_DEVERR_SEQLEN is set).
+ *   max_seq_len    : host-side upper bound of seq_lens.
+ *   scale          : softmax scale; 0 for the default 1/sqrt(d).
+ *   out_dev        : [total_q][Hq][128], fp16 (out_fp32 = 0) or fp32 (out_fp32 = 1); rows in
+ *                    no sequence are left as they were.  Must not overlap q or the workspace.
+ *   workspace_dev  : >= tq_chunk_workspace_bytes(...) bytes, 16-byte aligned.
+ * A cache row behind a sequence's last token may hold anything.  The launches are queued on
+ * stream, on the context's device; total_q = 0 or B = 0 launches nothing.
+ */
+TQ_API tq_status tq_chunk_attention(const tq_ctx* ctx, const uint16_t* q_dev, const int32_t* cu_q_dev,
+                                    const uint8_t* k_cache_dev, const uint8_t* v_cache_dev, int num_blocks,
+                                    const int32_t* block_table_dev, int max_blocks, const int32_t* seq_lens_dev, int B,
+                                    int total_q, int Hq, int Hkv, int max_seq_len, float scale, void* out_dev,
+                                    int out_fp32, void* workspace_dev, size_t workspace_bytes, void* stream);
+
+/*
  * Size of the device array behind tq_decode_attention_noalloc.  Every GPU that
  * loads libtq reserves this much device memory for it until the process exits.
  */

@@ -109,6 +109,8 @@ struct Args {
     long long v_stride;       // elements from one token to the next
     void* out;
     int out_fp32;
+    float* part;              // [splits][total_q * Hq][128] unscaled sums, or null: one split
+    float2* part_ml;          // [splits][total_q * Hq] maximum (base 2) and sum
     uint32_t* err;
 };
 
@@ -141,7 +143,7 @@ __global__ void __launch_bounds__(kAThreads, 1)
     // ---- which rows
     const int slot = (int)(blockIdx.x / (unsigned)a.heads), hk = (int)(blockIdx.x % (unsigned)a.heads);
     const int QC = 2 * a.QT;
-    if (blockIdx.x == 0) {  // the whole list is looked through once
+    if (blockIdx.x == 0 && blockIdx.y == 0) {  // the whole list is looked through once
         for (int b = threadIdx.x; b < a.B; b += kAThreads)
             if (a.cu_q[b] < 0 || a.cu_q[b + 1] < a.cu_q[b] || a.cu_q[b + 1] > a.total_q)
                 atomicOr(a.err, TQ_DEVERR_SEQLEN);
@@ -156,6 +158,7 @@ __global__ void __launch_bounds__(kAThreads, 1)
     const int kv_len = a.kv_lens ? a.kv_lens[b] : nq;
     const int off = kv_len - nq;
     if (off < 0 || (a.kv_lens && kv_len > a.max_kv)) {  // a length that cannot be: zero rows
+        if (blockIdx.y) return;
         if (threadIdx.x == 0) atomicOr(a.err, TQ_DEVERR_SEQLEN);
         const int rows = min(QC, nq - q0) * a.G;
         for (int i = threadIdx.x; i < rows * kDim; i += kAThreads) {
@@ -166,14 +169,28 @@ __global__ void __launch_bounds__(kAThreads, 1)
         }
         return;
     }
-    const int kv_row = a.kv_lens ? b * a.kv_pad : c0;  // row of the sequence's token 0
     // tiles of each half: up to its last query's position
     auto tiles_of = [&](int h) {
         const int first = q0 + h * a.QT;
         return first < nq ? (off + min(nq, first + a.QT) + kAN - 1) / kAN : 0;
     };
-    const int n0 = tiles_of(0), n1 = tiles_of(1), n = max(n0, n1);
-    const int masked_from = (off + q0 + 1) / kAN;  // first tile with a masked (row, token) pair
+    // this split's share of the tiles, j0 on (counts and tile numbers below are from j0)
+    const int all = max(tiles_of(0), tiles_of(1));
+    const int share = (all + (int)gridDim.y - 1) / (int)gridDim.y, j0 = min((int)blockIdx.y * share, all);
+    const int n0 = max(0, min(tiles_of(0) - j0, share)), n1 = max(0, min(tiles_of(1) - j0, share)), n = max(n0, n1);
+    const int masked_from = max((off + q0 + 1) / kAN - j0, 0);  // first tile with a masked (row, token) pair
+    if (n == 0) {  // nothing for this split
+        if (a.part) {
+            const int rows = min(QC, nq - q0) * a.G;
+            for (int r = threadIdx.x; r < rows; r += kAThreads)
+                a.part_ml[(size_t)blockIdx.y * a.total_q * a.Hq + (size_t)(c0 + q0 + r / a.G) * a.Hq +
+                          (a.head0 + hk) * a.G + r % a.G] = make_float2(-INFINITY, 0.f);
+        }
+        return;
+    }
+
+    // row of the split's token 0 (the sequence's token j0 * 128)
+    const int kv_row = (a.kv_lens ? b * a.kv_pad : c0) + j0 * kAN;
 
     const uint32_t bars = sbase + kAOffBar;
     auto bar = [&](int i) -> uint32_t { return bars + 8u * (uint32_t)i; };
@@ -362,8 +379,8 @@ __global__ void __launch_bounds__(kAThreads, 1)
         const uint32_t ts = tmem + h * 128 + lanes, to = tmem + 256 + h * 128 + lanes;
         const int qi = q0 + h * a.QT + row / a.G;           // this row's query
         const bool live = row < a.G * a.QT && qi < nq;
-        const int limit = live ? off + qi : -1;             // its last token
-        const int half_masked = (off + q0 + h * a.QT + 1) / kAN;
+        const int limit = live ? off + qi - j0 * kAN : -1;  // its last token
+        const int half_masked = (off + q0 + h * a.QT + 1) / kAN - j0;
         float m = -INFINITY, l = 0.f;
         bool ok = true;
         for (int j = 0; j < nh; ++j) {
@@ -377,7 +394,7 @@ __global__ void __launch_bounds__(kAThreads, 1)
 #pragma unroll
             for (int q = 0; q < 4; ++q) tmem_ld32(ts + 32 * q, s[q]);
             tmem_ld_wait();
-            const int okp = a.pages_ok ? a.pages_ok[(size_t)b * (a.kv_pad / kAN) + j] : 0xff;
+            const int okp = a.pages_ok ? a.pages_ok[(size_t)b * (a.kv_pad / kAN) + j0 + j] : 0xff;
             if (j >= half_masked || okp != 0xff) {
                 const int lim = limit - j * kAN;
 #pragma unroll
@@ -447,10 +464,12 @@ __global__ void __launch_bounds__(kAThreads, 1)
                 ok = false;
             }
         }
+        const size_t orow = (size_t)(c0 + qi) * a.Hq + (a.head0 + hk) * a.G + row % a.G;
+        const size_t prow = (size_t)blockIdx.y * a.total_q * a.Hq + orow;
+        if (a.part && live) a.part_ml[prow] = ok ? make_float2(m, l) : make_float2(-INFINITY, 0.f);
         if (ok && nh > 0) {
             tc_fence_after();
-            const float inv = l != 0.f ? 1.f / l : 0.f;  // (no token: a zero row)
-            const size_t orow = ((size_t)(c0 + qi) * a.Hq + (a.head0 + hk) * a.G + row % a.G) * kDim;
+            const float inv = a.part ? 1.f : l != 0.f ? 1.f / l : 0.f;  // (no token: a zero row)
             const bool fix = *repaired != 0;
 #pragma unroll 1
             for (int q = 0; q < 4; ++q) {
@@ -471,12 +490,13 @@ __global__ void __launch_bounds__(kAThreads, 1)
                         }
                     }
                 }
-                if (a.out_fp32) {
-                    float4* d = reinterpret_cast<float4*>(static_cast<float*>(a.out) + orow + 32 * q);
+                if (a.part || a.out_fp32) {
+                    float4* d = reinterpret_cast<float4*>(
+                        (a.part ? a.part + prow * kDim : static_cast<float*>(a.out) + orow * kDim) + 32 * q);
 #pragma unroll
                     for (int i = 0; i < 8; ++i) d[i] = make_float4(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]);
                 } else {
-                    uint4* d = reinterpret_cast<uint4*>(static_cast<__half*>(a.out) + orow + 32 * q);
+                    uint4* d = reinterpret_cast<uint4*>(static_cast<__half*>(a.out) + orow * kDim + 32 * q);
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         uint32_t w[4];
@@ -520,6 +540,8 @@ cudaError_t launch_attend(const tq_ctx* ctx, const AttendCall& c, cudaStream_t s
     a.v_stride = c.v_stride;
     a.out = c.out;
     a.out_fp32 = c.out_fp32;
+    a.part = c.splits > 1 ? c.part : nullptr;
+    a.part_ml = reinterpret_cast<float2*>(c.part_ml);
     a.err = ctx->dev_error;
     const long long kv_rows = c.kv_lens ? (long long)c.B * c.kv_pad : c.total_q;
     CUtensorMap mq, mk, mv;
@@ -532,7 +554,7 @@ cudaError_t launch_attend(const tq_ctx* ctx, const AttendCall& c, cudaStream_t s
     // slots of all sequences: floor(total / q) + B bounds every sequence's last one
     const long long slots = (long long)c.total_q / (2 * a.QT) + c.B;
     if (slots * c.heads > 0x7FFFFFFFll) return cudaErrorInvalidValue;
-    attend_tc_kernel<<<(unsigned)(slots * c.heads), kAThreads, kASmem, stream>>>(mq, mk, mv, a);
+    attend_tc_kernel<<<dim3((unsigned)(slots * c.heads), (unsigned)(c.splits > 1 ? c.splits : 1)), kAThreads, kASmem, stream>>>(mq, mk, mv, a);
     e = cudaGetLastError();
     if (e == cudaSuccess) count_launches(1);
     return e;

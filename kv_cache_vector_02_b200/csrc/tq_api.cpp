@@ -283,6 +283,12 @@ tq_status tq_init_ex(int head_dim, int bits, uint64_t seed, int rotation, int ke
     ctx->dev.Sh = base16 + 2 * n;
     ctx->dev.Rh = base16 + 3 * n;
     ctx->dev.Rl = base16 + 4 * n;
+    if (!tq::encode_rows_tmap(&ctx->map_Rh, ctx->dev.Rh, kDim) || !tq::encode_rows_tmap(&ctx->map_Sh, ctx->dev.Sh, kDim)) {
+        cudaFree(ctx->dev_block);
+        cudaFree(ctx->dev_error);
+        delete ctx;
+        return TQ_ERR_CUDA;
+    }
     ctx->tc.images = base8 + tc_off + tcb.off_images;
     ctx->tc.lut_value = base8 + tc_off + tcb.off_lut_value;
     ctx->tc.lut_key = base8 + tc_off + tcb.off_lut_key;
@@ -539,6 +545,59 @@ tq_status tq_prompt_attention(const tq_ctx* ctx, const uint16_t* q, int64_t q_st
     c.out_fp32 = out_fp32;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (tq::launch_attend(ctx, c, s) != cudaSuccess) return TQ_ERR_CUDA;
+    return note_use(ctx, s) ? TQ_OK : TQ_ERR_CUDA;
+}
+
+size_t tq_chunk_workspace_bytes(const tq_ctx* ctx, int B, int total_q, int Hq, int Hkv, int max_seq_len) {
+    if (!ctx || ctx->host_only || B < 1 || total_q < 0 || Hq < 1 || Hkv < 1 || max_seq_len < 0) return 0;
+    if (Hq % Hkv != 0 || Hq / Hkv > 128) return 0;
+    return tq::plan_chunk(ctx, B, total_q, Hq, Hkv, max_seq_len).bytes;
+}
+
+tq_status tq_chunk_attention(const tq_ctx* ctx, const uint16_t* q, const int32_t* cu_q, const uint8_t* k_cache,
+                             const uint8_t* v_cache, int num_blocks, const int32_t* block_table, int max_blocks,
+                             const int32_t* seq_lens, int B, int total_q, int Hq, int Hkv, int max_seq_len, float scale,
+                             void* out, int out_fp32, void* workspace, size_t workspace_bytes, void* stream) {
+    NvtxRange nvtx("tq_chunk_attention");
+    if (!ctx || ctx->host_only || B < 0 || total_q < 0 || Hq < 1 || Hkv < 1 || max_blocks < 0 || num_blocks < 0 ||
+        max_seq_len < 0)
+        return TQ_ERR_INVALID_ARG;
+    if (Hq % Hkv != 0 || Hq / Hkv > 128) return TQ_ERR_INVALID_ARG;
+    if (!(scale >= 0.f) || !std::isfinite(scale)) return TQ_ERR_INVALID_ARG;
+    if (B == 0 || total_q == 0) return TQ_OK;
+    if (!q || !cu_q || !k_cache || !v_cache || !block_table || !seq_lens || !out || !workspace)
+        return TQ_ERR_INVALID_ARG;
+    if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(out) || !aligned16(workspace))
+        return TQ_ERR_INVALID_ARG;
+    const tq::ChunkPlan plan = tq::plan_chunk(ctx, B, total_q, Hq, Hkv, max_seq_len);
+    if (plan.bytes == 0 || workspace_bytes < plan.bytes) return TQ_ERR_INVALID_ARG;
+    const long long out_bytes = (long long)total_q * Hq * kDim * (out_fp32 ? 4 : 2);
+    const Rows o{out, 1, out_bytes, out_bytes}, w{workspace, 1, (long long)plan.bytes, (long long)plan.bytes};
+    const Rows qr = fp16_rows(q, total_q, Hq, (int64_t)Hq * kDim);
+    if (overlap(o, qr) || overlap(o, w) || overlap(w, qr)) return TQ_ERR_INVALID_ARG;
+    if (scale == 0.f) scale = 1.0f / std::sqrt(float(kDim));
+    DeviceGuard dev(ctx->device);
+    if (!dev.ok) return TQ_ERR_CUDA;
+    tq::ChunkCall c{};
+    c.q = q;
+    c.cu_q = cu_q;
+    c.kc = k_cache;
+    c.vc = v_cache;
+    c.num_blocks = num_blocks;
+    c.block_table = block_table;
+    c.max_blocks = max_blocks;
+    c.seq_lens = seq_lens;
+    c.B = B;
+    c.total_q = total_q;
+    c.Hq = Hq;
+    c.Hkv = Hkv;
+    c.max_seq_len = max_seq_len;
+    c.scale = scale;
+    c.out = out;
+    c.out_fp32 = out_fp32;
+    c.workspace = static_cast<uint8_t*>(workspace);
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (tq::launch_chunk(ctx, plan, c, s) != cudaSuccess) return TQ_ERR_CUDA;
     return note_use(ctx, s) ? TQ_OK : TQ_ERR_CUDA;
 }
 

@@ -88,6 +88,7 @@ struct tq_ctx {
     tq::ChunkLayout lay_value{}, lay_key{};
     tq::DeviceParams dev{};
     tq::TcTables tc{};              // tensor-core compress operands and tables (in dev_block)
+    CUtensorMap map_Rh{}, map_Sh{}; // dev.Rh, dev.Sh as 128 x 128 operands
     void* dev_block = nullptr;      // all device parameters
     uint32_t* dev_error = nullptr;  // device error word
 };
@@ -167,8 +168,38 @@ struct AttendCall {
     float scale;
     void* out;
     int out_fp32;
+    int splits;              // > 1: over the tokens, into part and part_ml
+    float* part;             // fp32 [splits][total_q * Hq][128] unscaled sums
+    float* part_ml;          // fp32 [splits][total_q * Hq][2] maximum (base 2) and sum
 };
 cudaError_t launch_attend(const tq_ctx* ctx, const AttendCall& c, cudaStream_t stream);
+// A chunk call's way through its workspace (chunk.cu).
+struct ChunkPlan {
+    int kv_pad;          // tokens of a sequence, rounded up to whole tiles of 128
+    int heads;           // kv heads decompressed at a time
+    int splits;          // of the tokens, in the attention
+    size_t k_off, v_off; // workspace offsets (bytes): fp16 [B * kv_pad][heads][128]
+    size_t pages_off;    // u8 [B][kv_pad / 128]
+    size_t part_off, ml_off;
+    size_t bytes;
+};
+ChunkPlan plan_chunk(const tq_ctx* ctx, int B, int total_q, int Hq, int Hkv, int max_seq_len);
+struct ChunkCall {
+    const uint16_t* q;        // [total_q][Hq][128]
+    const int32_t* cu_q;      // [B + 1]
+    const uint8_t* kc;
+    const uint8_t* vc;
+    int num_blocks;
+    const int32_t* block_table;  // [B][max_blocks]
+    int max_blocks;
+    const int32_t* seq_lens;  // [B]
+    int B, total_q, Hq, Hkv, max_seq_len;
+    float scale;
+    void* out;
+    int out_fp32;
+    uint8_t* workspace;
+};
+cudaError_t launch_chunk(const tq_ctx* ctx, const ChunkPlan& plan, const ChunkCall& c, cudaStream_t stream);
 cudaError_t launch_decode(const tq_ctx* ctx, const DecodePlan& plan, const uint16_t* q, const uint8_t* kc,
                           const uint8_t* vc, int num_blocks, const int32_t* block_table, int max_blocks,
                           const int32_t* seq_lens, int B, int Hq, int Hkv, int max_seq_len, const DecodeTail& tail,

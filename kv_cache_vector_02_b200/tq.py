@@ -30,6 +30,7 @@ ROPE_SCALE_NONE, ROPE_SCALE_LINEAR, ROPE_SCALE_NTK, ROPE_SCALE_BANDS, ROPE_SCALE
 EXPORTED = ("tq_init", "tq_init_ex", "tq_init_host", "tq_destroy", "tq_chunk_bytes", "tq_code_bits", "tq_export_params", "tq_compress",
             "tq_decompress", "tq_decode_workspace_bytes", "tq_decode_attention", "tq_decode_attention_window",
             "tq_prefill_attention", "tq_rope_plan", "tq_rope", "tq_prompt_attention",
+            "tq_chunk_workspace_bytes", "tq_chunk_attention",
             "tq_decode_attention_noalloc",
             "tq_get_device_error", "tq_debug_stall", "tq_launch_count", "tq_status_string")
 
@@ -69,6 +70,8 @@ def _load():
         "tq_rope_plan": (I, [I, I, D, I, D, D, D, D, ctypes.POINTER(RopeTable)]),
         "tq_rope": (I, [ctypes.POINTER(RopeTable), P, I64, P, I64, I, I, I, P, P, I64, P, I64, I, P]),
         "tq_prompt_attention": (I, [P, P, I64, P, I64, P, I64, I, P, I, I, I, F, P, I, P]),
+        "tq_chunk_workspace_bytes": (Z, [P, I, I, I, I, I]),
+        "tq_chunk_attention": (I, [P, P, P, P, P, I, P, I, P, I, I, I, I, I, F, P, I, P, Z, P]),
         "tq_decode_attention_noalloc": (I, [P, P, P, P, I, P, I, P, I, I, I, I, F, P, I, P]),
         "tq_get_device_error": (I, [P, P, ctypes.POINTER(ctypes.c_uint32)]),
         "tq_debug_stall": (I, [P, I]),
@@ -397,6 +400,40 @@ def tq_prompt_attention(ctx: Context, q, k, v, cu_seqlens, out, scale: float = 0
     _check(_lib.tq_prompt_attention(ctx.handle, _ptr(q), sq, _ptr(k), sk, _ptr(v), sv, T, _ptr(cu_seqlens), B, Hq, Hkv,
                                     float(scale), _ptr(out), 1 if out.dtype == torch.float32 else 0,
                                     _stream_on(stream, q)), what)
+
+
+def tq_chunk_workspace_bytes(ctx: Context, B: int, total_q: int, Hq: int, Hkv: int, max_seq_len: int) -> int:
+    n = int(_lib.tq_chunk_workspace_bytes(ctx.handle, B, total_q, Hq, Hkv, max_seq_len))
+    if n == 0:
+        raise TQError(TQ_ERR_INVALID_ARG, "tq_chunk_workspace_bytes")
+    return n
+
+
+def tq_chunk_attention(ctx: Context, q, cu_q, k_cache, v_cache, block_table, seq_lens, max_seq_len: int, out, workspace,
+                       scale: float = 0.0, Hkv: int | None = None, stream=None):
+    """Causal attention of ragged chunks over the compressed cache: q [total_q, Hq, 128]
+    fp16, cu_q [B + 1] int32, block_table [B, max_blocks] int32, seq_lens [B] int32 (cached
+    tokens, the chunk's among them), out [total_q, Hq, 128] fp16 or fp32, workspace uint8
+    tensor of tq_chunk_workspace_bytes (see tq.h)."""
+    import torch
+    what = "tq_chunk_attention"
+    total_q, Hq = int(q.shape[0]), int(q.shape[1])
+    if Hkv is None:
+        Hkv = int(k_cache.shape[1])
+    _expect(q, (total_q, Hq, ctx.head_dim), (torch.float16,), what, "q")
+    _expect(k_cache, (None, Hkv, tq_chunk_bytes(ctx, KIND_KEY)), (torch.uint8,), what, "k_cache")
+    _expect(v_cache, (int(k_cache.shape[0]), Hkv, tq_chunk_bytes(ctx, KIND_VALUE)), (torch.uint8,), what, "v_cache")
+    _expect(seq_lens, (None,), (torch.int32,), what, "seq_lens")
+    B = int(seq_lens.shape[0])
+    _expect(block_table, (B, None), (torch.int32,), what, "block_table")
+    _expect(cu_q, (B + 1,), (torch.int32,), what, "cu_q")
+    _expect(out, (total_q, Hq, ctx.head_dim), (torch.float16, torch.float32), what, "out")
+    _expect(workspace, (None,), (torch.uint8,), what, "workspace")
+    _same_device(what, q, cu_q, k_cache, v_cache, block_table, seq_lens, out, workspace)
+    _check(_lib.tq_chunk_attention(ctx.handle, _ptr(q), _ptr(cu_q), _ptr(k_cache), _ptr(v_cache), int(k_cache.shape[0]),
+                                   _ptr(block_table), int(block_table.shape[1]), _ptr(seq_lens), B, total_q, Hq, Hkv,
+                                   int(max_seq_len), float(scale), _ptr(out), 1 if out.dtype == torch.float32 else 0,
+                                   _ptr(workspace), int(workspace.numel()), _stream_on(stream, q)), what)
 
 
 NOALLOC_SCRATCH_BYTES = 8 << 20

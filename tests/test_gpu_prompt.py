@@ -3,7 +3,7 @@ import math
 
 import pytest
 
-from attention64 import attend64, bound
+from attention64 import attend64, bound, rms_bound
 from parity import gpu_ctx, record
 
 pytestmark = pytest.mark.gpu
@@ -33,21 +33,24 @@ def _starts(lens, first=0):
 
 def _check(got, q, k, v, lens, label, first=0, scale=0.0, heads=None):
     import torch
-    at, worst = first, 0.0
+    at, worst, got2, may2 = first, 0.0, 0.0, 0.0
     hs = list(range(q.shape[1])) if heads is None else heads
     G = q.shape[1] // k.shape[1]
     for n in lens:
         if n:
             for h in hs:
                 sl = slice(at, at + n)
-                o, A, e = attend64(q[sl, h:h + 1].double(), k[sl, h // G:h // G + 1].double(),
+                o, A, e, V = attend64(q[sl, h:h + 1].double(), k[sl, h // G:h // G + 1].double(),
                                    v[sl, h // G:h // G + 1].double(), 0, scale)
-                b = bound(o, A, e, n, float(v[sl].abs().max()), got.dtype == torch.float16)
+                b = bound(o, A, e, V, n, float(v[sl].abs().max()), got.dtype == torch.float16)
                 err = (got[sl, h:h + 1].double() - o).abs()
                 worst = max(worst, float((err / b).max()))
+                got2 += float(err.square().sum())
+                may2 += float(rms_bound(A, q[sl, h:h + 1].double(), k[sl, h // G:h // G + 1].double(), 1, scale).square().sum())
                 assert bool((err <= b).all()), (label, h, n, float((err / b).max()), int((err > b).sum()))
         at += n
-    record(label, {"max_err_over_bound": worst})
+    record(label, {"max_err_over_bound": worst, "rms_over_bound": math.sqrt(got2 / max(may2, 1e-30))})
+    assert got2 <= may2, (label, math.sqrt(got2 / may2))
 
 
 @pytest.mark.parametrize("lens,Hq,Hkv,fp32,loud", [
