@@ -8,14 +8,16 @@
 // One CTA per (256 rows, kv head).  A row is a (query, query head of the group) pair, the
 // group's G heads packed beside each other, so keys and values are read once for all of
 // them and a causal tile's waste is that of 128 / G queries, not of 128.  The rows are two
-// halves of 128 (one TMEM lane each); the halves take turns, one half's softmax running
-// while the tensor core works for the other:
+// halves of 128 (one TMEM lane each); each has its own softmax warps:
 //   warps 0-3, 4-7  softmax of half 0, 1: one thread per row.  Scores come from tensor
 //                   memory into registers, the running maximum and sum are fp32, base 2;
 //                   P goes back over the scores' own columns as packed fp16
-//   warp 8          MMA issuer (one thread): S = Q K^T (A, B in shared memory),
+//   warp 8          MMA issuer: S = Q K^T (A, B in shared memory),
 //                   O += P V (A in tensor memory, V as it lies: N-major descriptor)
 //   warp 9          TMA producer: Q once, then rings of K and V tiles of 128 tokens
+// A half's scores come in steps of 64 tokens through two buffers, so that its softmax finds
+// the next step's scores ready and never waits for the tensor core; with one buffer of 128
+// tokens the two took turns, at 26 % of the tensor pipe and 27 % of the exponentials' pipe.
 //   warps 10, 11    masked tiles only: clear what is not finite in V (below)
 // O is rescaled only when a row's maximum has grown by more than 2^8 since the one it is
 // scaled by: P stays below 2^8, far inside fp16, and the sum is exact about it either way.
@@ -36,6 +38,7 @@ namespace {
 using namespace sm100;
 
 constexpr int kAN = 128;                    // tokens of a tile
+constexpr int kAS = 64;                     // tokens of a step
 constexpr uint32_t kATile = 128 * kDim * 2;  // one 128 x 128 fp16 operand
 constexpr uint32_t kAHalf = kATile / 2;      // 64 of its columns
 constexpr int kAKStages = 3, kAVStages = 2;
@@ -55,19 +58,26 @@ enum : int {
     kABKEmpty = 4,   // +stage
     kABVFull = 7,    // +stage
     kABVEmpty = 9,   // +stage
-    kABVClean = 11,  // +stage: a masked tile has been looked through
-    kABS = 13,       // +half: scores in tensor memory (and the half's earlier MMAs done)
-    kABP = 15,       // +half: P in tensor memory
-    kABO = 17,       // +half: every MMA of the half done
-    kABDrain = 19,
-    kABVGo = 20,     // +stage: a masked tile's load has been issued
-    kANumBars = 22
+    kABVGo = 11,     // +stage: a masked tile's load has been issued
+    kABVClean = 13,  // +stage: a masked tile has been looked through
+    kABS = 15,       // +2 half + buffer: scores in tensor memory
+    kABP = 19,       // +2 half + buffer: P in tensor memory
+    kABO = 23,       // +half: a step's P V added (and everything issued before it)
+    kABDrain = 25,
+    kANumBars = 26
 };
 
 __device__ __forceinline__ float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
+}
+
+// The largest of three.
+__device__ __forceinline__ float max3(float x, float y, float z) {
+    float m;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(m) : "f"(x), "f"(y), "f"(z));
+    return m;
 }
 
 __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
@@ -135,7 +145,7 @@ __global__ void __launch_bounds__(kAThreads, 1)
                      const __grid_constant__ CUtensorMap tv_map, const Args a) {
     extern __shared__ __align__(1024) uint8_t smem[];
     const uint32_t sbase = smem_u32(smem);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;  // (warp: uniform)
     if (sbase & 1023u) {
         if (threadIdx.x == 0) atomicOr(a.err, TQ_DEVERR_INTERNAL);
         return;
@@ -169,15 +179,16 @@ __global__ void __launch_bounds__(kAThreads, 1)
         }
         return;
     }
-    // tiles of each half: up to its last query's position
-    auto tiles_of = [&](int h) {
+    // steps of each half: up to its last query's position
+    auto steps_of = [&](int h) {
         const int first = q0 + h * a.QT;
-        return first < nq ? (off + min(nq, first + a.QT) + kAN - 1) / kAN : 0;
+        return first < nq ? (off + min(nq, first + a.QT) + kAS - 1) / kAS : 0;
     };
-    // this split's share of the tiles, j0 on (counts and tile numbers below are from j0)
-    const int all = max(tiles_of(0), tiles_of(1));
+    // this split's share of the tiles, j0 on (counts, steps and tiles below are from there)
+    const int all = (max(steps_of(0), steps_of(1)) + 1) / 2;
     const int share = (all + (int)gridDim.y - 1) / (int)gridDim.y, j0 = min((int)blockIdx.y * share, all);
-    const int n0 = max(0, min(tiles_of(0) - j0, share)), n1 = max(0, min(tiles_of(1) - j0, share)), n = max(n0, n1);
+    const int n0 = max(0, min(steps_of(0) - 2 * j0, 2 * share)), n1 = max(0, min(steps_of(1) - 2 * j0, 2 * share));
+    const int n = max(n0, n1), nt = (n + 1) / 2;
     const int masked_from = max((off + q0 + 1) / kAN - j0, 0);  // first tile with a masked (row, token) pair
     if (n == 0) {  // nothing for this split
         if (a.part) {
@@ -213,11 +224,12 @@ __global__ void __launch_bounds__(kAThreads, 1)
             mbar_init(bar(kABVClean + s), 2);
             mbar_init(bar(kABVGo + s), 1);
         }
-        for (int h = 0; h < 2; ++h) {
-            mbar_init(bar(kABS + h), 1);
-            mbar_init(bar(kABP + h), 4);
-            mbar_init(bar(kABO + h), 1);
+        for (int i = 0; i < 4; ++i) {
+            mbar_init(bar(kABS + i), 1);
+            mbar_init(bar(kABP + i), 4);
         }
+        mbar_init(bar(kABO), 1);
+        mbar_init(bar(kABO + 1), 1);
         mbar_init(bar(kABDrain), 1);
         *abort = 0;
         *repaired = 0;
@@ -227,11 +239,16 @@ __global__ void __launch_bounds__(kAThreads, 1)
         tmem_alloc(smem_u32(tmem_slot), 512);
         tmem_relinquish();
     }
+    // pages that cannot be used among this split's (seldom: looked up per step only then)
+    bool bad_page = false;
+    const uint8_t* pages_ok = a.pages_ok ? a.pages_ok + (size_t)b * (a.kv_pad / kAN) + j0 : nullptr;
+    if (pages_ok)
+        for (int j = threadIdx.x; j < nt; j += kAThreads) bad_page |= pages_ok[j] != 0xff;
     tc_fence_before();
-    __syncthreads();
+    bad_page = __syncthreads_or(bad_page);
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    // columns: S0 (P0 over it) | S1 (P1) | O0 | O1
+    // columns: half 0's score buffers (64 each, P over a buffer's first 32) | half 1's | O0 | O1
 
     if (warp == 9) {
         // ------------------------------------------------------------ producer
@@ -256,8 +273,8 @@ __global__ void __launch_bounds__(kAThreads, 1)
             };
             bool ok = load(&tk_map, kABKFull, kABKEmpty, kAOffK, kAKStages, 0);
             kj = ok;
-            for (int j = 0; ok && j < n; ++j) {
-                if (j + 1 < n) {
+            for (int j = 0; ok && j < nt; ++j) {
+                if (j + 1 < nt) {
                     ok = load(&tk_map, kABKFull, kABKEmpty, kAOffK, kAKStages, j + 1);
                     kj += ok;
                 }
@@ -278,65 +295,86 @@ __global__ void __launch_bounds__(kAThreads, 1)
         __syncwarp();
     } else if (warp == 8) {
         // ------------------------------------------------------------ MMA issuer
-        if (lane == 0) {
-            const uint32_t id_s = idesc_f16(128, kAN), id_o = idesc_f16(128, kDim) | (1u << 16);
-            auto wait = [&](int i, int phase) -> bool {
-                if (mbar_wait(bar(i), (uint32_t)phase & 1u, abort, kAWaitNs)) return true;
-                give_up();
-                return false;
-            };
-            auto scores = [&](int h, int j) {
-                const uint32_t qa = sw128_desc_lo(sbase + kAOffQ + h * kATile);
-                const uint32_t kb = sw128_desc_lo(sbase + kAOffK + (j % kAKStages) * kATile);
+        // (the whole warp, converged: see umma_ss_warp; all 512 columns are ours, from 0 on)
+        constexpr uint32_t id_s = idesc_f16(128, kAS), id_o = idesc_f16(128, kDim) | (1u << 16);
+        const uint32_t q_lo = sw128_desc_lo(sbase + kAOffQ), k_lo = sw128_desc_lo(sbase + kAOffK);
+        const uint32_t v_lo = v_desc_lo(sbase + kAOffV);
+        auto wait = [&](int i, uint32_t parity) -> bool {
+            if (mbar_wait_all(bar(i), parity & 1u, abort, kAWaitNs)) return true;
+            if (lane == 0) give_up();
+            return false;
+        };
+        // scores of half h into its buffer u: the u-th 64 keys of the tile in `stage`
+        auto scores = [&](int h, int u, int stage) {
+            const uint32_t ql = q_lo + h * (kATile >> 4), kl = k_lo + stage * (kATile >> 4) + u * (kAS * 128 >> 4);
 #pragma unroll
-                for (int ks = 0; ks < 8; ++ks) {
-                    const uint32_t o = (uint32_t)(ks & 3) * 2 + (uint32_t)(ks >> 2) * (kAHalf >> 4);
-                    umma_ss(tmem + h * 128, sw128_desc(qa + o), sw128_desc(kb + o), id_s, ks > 0);
-                }
-                umma_commit(bar(kABS + h));
-            };
-            auto values = [&](int h, int j) {
-                const uint32_t vb = v_desc_lo(sbase + kAOffV + (j % kAVStages) * kATile);
+            for (int ks = 0; ks < 8; ++ks) {
+                const uint32_t o = (uint32_t)(ks & 3) * 2 + (uint32_t)(ks >> 2) * (kAHalf >> 4);
+                umma_ss_warp(h * 128 + u * kAS, sw128_desc(ql + o), sw128_desc(kl + o), id_s, ks > 0);
+            }
+            umma_commit_warp(bar(kABS + 2 * h + u));
+        };
+        auto values = [&](int h, int u, int stage, bool first) {
+            const uint32_t vl = v_lo + stage * (kATile >> 4) + u * (kAS * 128 >> 4);
 #pragma unroll
-                for (int ks = 0; ks < 8; ++ks)
-                    umma_ts(tmem + 256 + h * 128, tmem + h * 128 + ks * 8, sw128_desc(vb + ks * (2048 >> 4)), id_o,
-                            (j | ks) > 0);
-            };
-            bool ok = wait(kABQ, 0) && wait(kABKFull, 0);
-            if (ok) {
-                tc_fence_after();
-                if (n0) scores(0, 0);
-                if (n1) scores(1, 0);
-                umma_commit(bar(kABKEmpty));
-            }
-            for (int j = 0; ok && j < n; ++j) {
-                const int vs = j % kAVStages;
-                ok = j >= masked_from ? wait(kABVClean + vs, (j - masked_from) / kAVStages) : wait(kABVFull + vs, j / kAVStages);
-                if (ok && j + 1 < n) ok = wait(kABKFull + (j + 1) % kAKStages, (j + 1) / kAKStages);
-                for (int h = 0; ok && h < 2; ++h) {
-                    const int nh = h ? n1 : n0;
-                    if (j >= nh) continue;
-                    ok = wait(kABP + h, j);
-                    if (!ok) break;
-                    tc_fence_after();
-                    values(h, j);
-                    if (j + 1 < nh) scores(h, j + 1);
-                    else umma_commit(bar(kABO + h));
-                }
-                if (ok) {
-                    umma_commit(bar(kABVEmpty + vs));
-                    if (j + 1 < n) umma_commit(bar(kABKEmpty + (j + 1) % kAKStages));
-                }
-            }
-            // nothing is in flight when the CTA exits
-            umma_commit(bar(kABDrain));
-            const volatile int never = 0;
-            mbar_wait(bar(kABDrain), 0, &never, kAWaitNs);
+            for (int ks = 0; ks < 4; ++ks)
+                umma_ts_warp(256 + h * 128, h * 128 + u * kAS + ks * 8, sw128_desc(vl + ks * (2048 >> 4)), id_o,
+                             !(first && ks == 0));
+            umma_commit_warp(bar(kABO + h));
+        };
+        bool ok = tmem == 0;
+        if (!ok && lane == 0) {
+            *abort = 1;
+            atomicOr(a.err, TQ_DEVERR_INTERNAL);
         }
+        ok = ok && wait(kABQ, 0) && wait(kABKFull, 0);
+        if (ok) {
+            tc_fence_after();
+#pragma unroll
+            for (int u = 0; u < 2; ++u)
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    if (u < (h ? n1 : n0)) scores(h, u, 0);
+            umma_commit_warp(bar(kABKEmpty));
+        }
+        int vs = 0, kn = 0;          // stages of tile j's values and of tile j + 1's keys
+        uint32_t vp = 0, kp = 0;     // and their phases
+        for (int j = 0; ok && j < nt; ++j) {
+            if (++kn == kAKStages) {
+                kn = 0;
+                kp ^= 1u;
+            }
+            ok = j >= masked_from ? wait(kABVClean + vs, (j - masked_from) / kAVStages) : wait(kABVFull + vs, vp);
+            if (ok && j + 1 < nt) ok = wait(kABKFull + kn, kp);
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int nh = h ? n1 : n0, i = 2 * j + u;
+                    if (!ok || i >= nh) continue;
+                    ok = wait(kABP + 2 * h + u, j);
+                    if (!ok) continue;
+                    tc_fence_after();
+                    values(h, u, vs, i == 0);
+                    if (i + 2 < nh) scores(h, u, kn);
+                }
+            }
+            if (!ok) break;
+            umma_commit_warp(bar(kABVEmpty + vs));
+            if (j + 1 < nt) umma_commit_warp(bar(kABKEmpty + kn));
+            if (++vs == kAVStages) {
+                vs = 0;
+                vp ^= 1u;
+            }
+        }
+        // nothing is in flight when the CTA exits
+        umma_commit_warp(bar(kABDrain));
+        const volatile int never = 0;
+        mbar_wait(bar(kABDrain), 0, &never, kAWaitNs);
         __syncwarp();
     } else if (warp >= 10) {
         // ------------------------------------------------------------ masked tiles' values
-        for (int j = masked_from; j < n; ++j) {
+        for (int j = masked_from; j < nt; ++j) {
             const int s = j % kAVStages;
             // (these warps do not follow the unmasked tiles' phases of the stage: its load's
             // issue tells them that the phase of this tile is the current one)
@@ -380,43 +418,61 @@ __global__ void __launch_bounds__(kAThreads, 1)
         const int qi = q0 + h * a.QT + row / a.G;           // this row's query
         const bool live = row < a.G * a.QT && qi < nq;
         const int limit = live ? off + qi - j0 * kAN : -1;  // its last token
-        const int half_masked = (off + q0 + h * a.QT + 1) / kAN - j0;
-        float m = -INFINITY, l = 0.f;
+        const int half_masked = (off + q0 + h * a.QT + 1) / kAS - 2 * j0;  // first step with a masked pair
+        const float2 sc = make_float2(a.scale_log2, a.scale_log2);
+        float m = -INFINITY;
+        float2 sum[2] = {{0.f, 0.f}, {0.f, 0.f}};
         bool ok = true;
-        for (int j = 0; j < nh; ++j) {
-            if (!mbar_wait_warp(bar(kABS + h), (uint32_t)j & 1u, abort, kAWaitNs)) {
-                give_up();
-                ok = false;
-                break;
-            }
+        auto wait = [&](int x, int phase) -> bool {
+            if (mbar_wait_all(bar(x), (uint32_t)phase & 1u, abort, kAWaitNs)) return true;
+            give_up();
+            return false;
+        };
+        for (int i = 0; i < nh; ++i) {
+            const uint32_t tb = ts + (i & 1) * kAS;
+            ok = wait(kABS + 2 * h + (i & 1), i / 2);
+            if (!ok) break;
             tc_fence_after();
-            uint32_t s[4][32];
-#pragma unroll
-            for (int q = 0; q < 4; ++q) tmem_ld32(ts + 32 * q, s[q]);
+            uint32_t s[2][32];
+            tmem_ld32(tb, s[0]);
+            tmem_ld32(tb + 32, s[1]);
             tmem_ld_wait();
-            const int okp = a.pages_ok ? a.pages_ok[(size_t)b * (a.kv_pad / kAN) + j0 + j] : 0xff;
-            if (j >= half_masked || okp != 0xff) {
-                const int lim = limit - j * kAN;
+            if (i >= half_masked) {
+                const int lim = limit - i * kAS;
 #pragma unroll
-                for (int q = 0; q < 4; ++q)
+                for (int q = 0; q < 2; ++q)
 #pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        if (32 * q + i > lim || !((okp >> (2 * q + i / 16)) & 1)) s[q][i] = 0xFF800000u;  // -inf
+                    for (int e = 0; e < 32; ++e)
+                        if (32 * q + e > lim) s[q][e] = 0xFF800000u;  // -inf
+            }
+            if (bad_page) {
+                const int okp = pages_ok[i / 2] >> (4 * (i & 1));
+#pragma unroll
+                for (int q = 0; q < 2; ++q)
+#pragma unroll
+                    for (int e = 0; e < 32; ++e)
+                        if (!((okp >> (2 * q + e / 16)) & 1)) s[q][e] = 0xFF800000u;
             }
             float mx[4];
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-                mx[q] = __uint_as_float(s[q][0]);
+                const uint32_t* x = &s[q / 2][16 * (q & 1)];
+                mx[q] = max3(__uint_as_float(x[0]), __uint_as_float(x[1]), __uint_as_float(x[2]));
 #pragma unroll
-                for (int i = 1; i < 32; ++i) mx[q] = fmaxf(mx[q], __uint_as_float(s[q][i]));
+                for (int e = 3; e < 15; e += 2) mx[q] = max3(mx[q], __uint_as_float(x[e]), __uint_as_float(x[e + 1]));
+                mx[q] = fmaxf(mx[q], __uint_as_float(x[15]));
             }
-            const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * a.scale_log2;
+            const float top = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * a.scale_log2;
             const bool grow = top > m + kRescale || (m == -INFINITY && top > m);
             if (__any_sync(0xffffffffu, grow)) {
                 const float mn = grow ? top : m;
-                if (j > 0) {
+                if (i > 0) {
                     const float f = grow ? ex2(m - mn) : 1.f;  // (first maximum: ex2(-inf) = 0)
-                    l *= f;
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) sum[q] = __fmul2_rn(sum[q], make_float2(f, f));
+                    ok = wait(kABO + h, i - 1);  // the step before is in O
+                    if (!ok) break;
+                    tc_fence_after();
 #pragma unroll
                     for (int q = 0; q < 8; ++q) {
                         uint32_t o[16];
@@ -424,9 +480,9 @@ __global__ void __launch_bounds__(kAThreads, 1)
                         tmem_ld_wait();
                         uint32_t lo[8], hi[8];
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            lo[i] = __float_as_uint(__uint_as_float(o[i]) * f);
-                            hi[i] = __float_as_uint(__uint_as_float(o[8 + i]) * f);
+                        for (int e = 0; e < 8; ++e) {
+                            lo[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                            hi[e] = __float_as_uint(__uint_as_float(o[8 + e]) * f);
                         }
                         tmem_st8(to + 16 * q, lo);
                         tmem_st8(to + 16 * q + 8, hi);
@@ -435,35 +491,27 @@ __global__ void __launch_bounds__(kAThreads, 1)
                 m = mn;
             }
             const float mm = m == -INFINITY ? 0.f : m;
-            float2 sum[2] = {{0.f, 0.f}, {0.f, 0.f}};
-            const float2 sc = make_float2(a.scale_log2, a.scale_log2), nm = make_float2(-mm, -mm);
+            const float2 nm = make_float2(-mm, -mm);
+            uint32_t p[32];
 #pragma unroll
-            for (int q = 0; q < 2; ++q) {
-                uint32_t p[32];
-#pragma unroll
-                for (int i = 0; i < 32; ++i) {
-                    const int e = 64 * q + 2 * i;
-                    float2 x = make_float2(__uint_as_float(s[e / 32][e % 32]), __uint_as_float(s[e / 32][e % 32 + 1]));
-                    x = __ffma2_rn(x, sc, nm);
-                    x.x = ex2(x.x);
-                    x.y = ex2(x.y);
-                    sum[i & 1] = __fadd2_rn(sum[i & 1], x);
-                    const __half2 hp = __floats2half2_rn(x.x, x.y);
-                    p[i] = *reinterpret_cast<const uint32_t*>(&hp);
-                }
-                tmem_st32(ts + 32 * q, p);
+            for (int e = 0; e < 32; ++e) {
+                float2 x = make_float2(__uint_as_float(s[e / 16][2 * e % 32]), __uint_as_float(s[e / 16][2 * e % 32 + 1]));
+                x = __ffma2_rn(x, sc, nm);
+                x.x = ex2(x.x);
+                x.y = ex2(x.y);
+                sum[e & 1] = __fadd2_rn(sum[e & 1], x);
+                const __half2 hp = __floats2half2_rn(x.x, x.y);
+                p[e] = *reinterpret_cast<const uint32_t*>(&hp);
             }
-            l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+            tmem_st32(tb, p);
             tmem_st_wait();
             tc_fence_before();
-            mbar_arrive_warp(bar(kABP + h));
+            mbar_arrive_warp(bar(kABP + 2 * h + (i & 1)));
         }
-        if (ok && nh > 0) {
-            if (!mbar_wait_warp(bar(kABO + h), 0, abort, kAWaitNs)) {
-                give_up();
-                ok = false;
-            }
-        }
+        // the last two steps' sums, in order (the scores of step i say that step i - 2 is in O)
+        if (ok && nh > 1) ok = wait(kABO + h, nh - 2);
+        if (ok && nh > 0) ok = wait(kABO + h, nh - 1);
+        const float l = (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
         const size_t orow = (size_t)(c0 + qi) * a.Hq + (a.head0 + hk) * a.G + row % a.G;
         const size_t prow = (size_t)blockIdx.y * a.total_q * a.Hq + orow;
         if (a.part && live) a.part_ml[prow] = ok ? make_float2(m, l) : make_float2(-INFINITY, 0.f);

@@ -93,7 +93,7 @@ __global__ void __launch_bounds__(kUThreads, 1)
                      const UnpackArgs a) {
     extern __shared__ __align__(1024) uint8_t smem[];
     const uint32_t sbase = smem_u32(smem);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;  // (warp: uniform)
     if (sbase & 1023u) {
         if (threadIdx.x == 0) atomicOr(a.err, TQ_DEVERR_INTERNAL);
         return;
@@ -211,41 +211,44 @@ __global__ void __launch_bounds__(kUThreads, 1)
         }
     } else if (warp == 8) {
         // ------------------------------------------------------------ MMA issuer
-        if (lane == 0) {
-            const uint32_t id_k = idesc_f16(128, kDim), id_n = id_k | (1u << 16);
-            auto wait = [&](int x, int phase) {
-                if (mbar_wait(bar(x), (uint32_t)phase & 1u, abort, kUWaitNs)) return true;
-                give_up();
-                return false;
-            };
-            const uint32_t A = sw128_desc_lo(sbase + kUOffA), R = sw128_desc_lo(sbase + kUOffR);
-            // S[j][i] with the output coordinate i contiguous: 64-coordinate blocks kUHalf apart
-            const uint32_t S = (((sbase + kUOffS) >> 4) & 0x3FFFu) | ((kUHalf >> 4) << 16);
-            long long i = blockIdx.x;
-            Item it;
-            bool ok = wait(kUBConst, 0);
-            int issued = 0;
-            for (int k = 0; ok && next(i, it); ++k, i += gridDim.x) {
-                ok = wait(kUBA, k) && (k == 0 || wait(kUBDEmpty, k - 1));
-                if (!ok) break;
-                ++issued;
-                tc_fence_after();
-#pragma unroll
-                for (int ks = 0; ks < 8; ++ks) {
-                    const uint32_t o = (uint32_t)(ks & 3) * 2 + (uint32_t)(ks >> 2) * (kUHalf >> 4);
-                    umma_ss(tmem, sw128_desc(A + o), sw128_desc(R + o), id_k, ks > 0);
-                    if (PROD)
-                        umma_ss(tmem + 128, sw128_desc(A + (kUTile >> 4) + o), sw128_desc(S + ks * (2048 >> 4)), id_n,
-                                ks > 0);
-                    umma_ss(tmem + 256, sw128_desc(A + 2 * (kUTile >> 4) + o), sw128_desc(R + o), id_k, ks > 0);
-                }
-                umma_commit(bar(kUBD));
-            }
-            // the operand matrices have landed and no MMA is in flight when the CTA exits
-            const volatile int never = 0;
-            mbar_wait(bar(kUBConst), 0, &never, kUWaitNs);
-            if (issued > 0) mbar_wait(bar(kUBD), (uint32_t)(issued - 1) & 1u, &never, kUWaitNs);
+        // (the whole warp, converged: see umma_ss_warp; all 512 columns are ours, from 0 on)
+        constexpr uint32_t id_k = idesc_f16(128, kDim), id_n = id_k | (1u << 16);
+        auto wait = [&](int x, int phase) {
+            if (mbar_wait_all(bar(x), (uint32_t)phase & 1u, abort, kUWaitNs)) return true;
+            if (lane == 0) give_up();
+            return false;
+        };
+        const uint32_t A = sw128_desc_lo(sbase + kUOffA), R = sw128_desc_lo(sbase + kUOffR);
+        // S[j][i] with the output coordinate i contiguous: 64-coordinate blocks kUHalf apart
+        const uint32_t S = (((sbase + kUOffS) >> 4) & 0x3FFFu) | ((kUHalf >> 4) << 16);
+        long long i = blockIdx.x;
+        Item it;
+        bool ok = tmem == 0;
+        if (!ok && lane == 0) {
+            *abort = 1;
+            atomicOr(a.err, TQ_DEVERR_INTERNAL);
         }
+        ok = ok && wait(kUBConst, 0);
+        int issued = 0;
+        for (int k = 0; ok && next(i, it); ++k, i += gridDim.x) {
+            ok = wait(kUBA, k) && (k == 0 || wait(kUBDEmpty, k - 1));
+            if (!ok) break;
+            ++issued;
+            tc_fence_after();
+#pragma unroll
+            for (int ks = 0; ks < 8; ++ks) {
+                const uint32_t o = (uint32_t)(ks & 3) * 2 + (uint32_t)(ks >> 2) * (kUHalf >> 4);
+                umma_ss_warp(0, sw128_desc(A + o), sw128_desc(R + o), id_k, ks > 0);
+                if (PROD)
+                    umma_ss_warp(128, sw128_desc(A + (kUTile >> 4) + o), sw128_desc(S + ks * (2048 >> 4)), id_n, ks > 0);
+                umma_ss_warp(256, sw128_desc(A + 2 * (kUTile >> 4) + o), sw128_desc(R + o), id_k, ks > 0);
+            }
+            umma_commit_warp(bar(kUBD));
+        }
+        // the operand matrices have landed and no MMA is in flight when the CTA exits
+        const volatile int never = 0;
+        mbar_wait(bar(kUBConst), 0, &never, kUWaitNs);
+        if (issued > 0) mbar_wait(bar(kUBD), (uint32_t)(issued - 1) & 1u, &never, kUWaitNs);
         __syncwarp();
     } else {
         // ------------------------------------------------------------ scale, round, store
