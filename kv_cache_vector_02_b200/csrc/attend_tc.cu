@@ -11,14 +11,14 @@
 // halves of 128 (one TMEM lane each); each has its own softmax warps:
 //   warps 0-3, 4-7  softmax of half 0, 1: one thread per row.  Scores come from tensor
 //                   memory into registers, the running maximum and sum are fp32, base 2;
-//                   P goes back over the scores' own columns as packed fp16
+//                   P goes to tensor memory as packed fp16
 //   warp 8          MMA issuer: S = Q K^T (A, B in shared memory),
 //                   O += P V (A in tensor memory, V as it lies: N-major descriptor)
 //   warp 9          TMA producer: Q once, then rings of K and V tiles of 128 tokens
-// A half's scores come in steps of 64 tokens through two buffers, so that its softmax finds
-// the next step's scores ready and never waits for the tensor core; with one buffer of 128
-// tokens the two took turns, at 26 % of the tensor pipe and 27 % of the exponentials' pipe.
-//   warps 10, 11    masked tiles only: clear what is not finite in V (below)
+// Tensor memory has no room for both halves' scores beside their P and O (640 columns of
+// 512), but scores are there only until their softmax has them in registers: the halves
+// share one score buffer in turn, and P has columns of its own.  So the next scores are
+// computed while the softmax before them runs, and no softmax waits for the tensor core.
 // O is rescaled only when a row's maximum has grown by more than 2^8 since the one it is
 // scaled by: P stays below 2^8, far inside fp16, and the sum is exact about it either way.
 //
@@ -38,11 +38,13 @@ namespace {
 using namespace sm100;
 
 constexpr int kAN = 128;                    // tokens of a tile
-constexpr int kAS = 64;                     // tokens of a step
 constexpr uint32_t kATile = 128 * kDim * 2;  // one 128 x 128 fp16 operand
 constexpr uint32_t kAHalf = kATile / 2;      // 64 of its columns
 constexpr int kAKStages = 3, kAVStages = 2;
 constexpr int kAThreads = 384;
+// Registers: 168 a thread at launch (the launch checks it), moved from warps 8-11 to the softmax.
+constexpr int kARegs = 168, kASoftmaxRegs = 200, kAOtherRegs = 104;
+static_assert(2 * kASoftmaxRegs + kAOtherRegs == 3 * kARegs, "the block's own registers");
 constexpr uint32_t kAOffQ = 0;
 constexpr uint32_t kAOffK = 2 * kATile;
 constexpr uint32_t kAOffV = kAOffK + kAKStages * kATile;
@@ -60,11 +62,12 @@ enum : int {
     kABVEmpty = 9,   // +stage
     kABVGo = 11,     // +stage: a masked tile's load has been issued
     kABVClean = 13,  // +stage: a masked tile has been looked through
-    kABS = 15,       // +2 half + buffer: scores in tensor memory
-    kABP = 19,       // +2 half + buffer: P in tensor memory
-    kABO = 23,       // +half: a step's P V added (and everything issued before it)
-    kABDrain = 25,
-    kANumBars = 26
+    kABS = 15,       // +half: the half's scores in the buffer
+    kABL = 17,       // +half: the half has them in registers
+    kABP = 19,       // +half: P in tensor memory
+    kABO = 21,       // +half: P V added
+    kABDrain = 23,
+    kANumBars = 24
 };
 
 __device__ __forceinline__ float ex2(float x) {
@@ -73,11 +76,20 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
-// The largest of three.
+// The largest of three; NaN if one is.
 __device__ __forceinline__ float max3(float x, float y, float z) {
     float m;
-    asm("max.f32 %0, %1, %2, %3;" : "=f"(m) : "f"(x), "f"(y), "f"(z));
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(m) : "f"(x), "f"(y), "f"(z));
     return m;
+}
+
+template <int N>
+__device__ __forceinline__ void set_registers_up() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void set_registers_down() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
 __device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
@@ -179,16 +191,15 @@ __global__ void __launch_bounds__(kAThreads, 1)
         }
         return;
     }
-    // steps of each half: up to its last query's position
-    auto steps_of = [&](int h) {
+    // tiles of each half: up to its last query's position
+    auto tiles_of = [&](int h) {
         const int first = q0 + h * a.QT;
-        return first < nq ? (off + min(nq, first + a.QT) + kAS - 1) / kAS : 0;
+        return first < nq ? (off + min(nq, first + a.QT) + kAN - 1) / kAN : 0;
     };
-    // this split's share of the tiles, j0 on (counts, steps and tiles below are from there)
-    const int all = (max(steps_of(0), steps_of(1)) + 1) / 2;
+    // this split's share of the tiles, j0 on (counts and tile numbers below are from there)
+    const int all = max(tiles_of(0), tiles_of(1));
     const int share = (all + (int)gridDim.y - 1) / (int)gridDim.y, j0 = min((int)blockIdx.y * share, all);
-    const int n0 = max(0, min(steps_of(0) - 2 * j0, 2 * share)), n1 = max(0, min(steps_of(1) - 2 * j0, 2 * share));
-    const int n = max(n0, n1), nt = (n + 1) / 2;
+    const int n0 = max(0, min(tiles_of(0) - j0, share)), n1 = max(0, min(tiles_of(1) - j0, share)), n = max(n0, n1);
     const int masked_from = max((off + q0 + 1) / kAN - j0, 0);  // first tile with a masked (row, token) pair
     if (n == 0) {  // nothing for this split
         if (a.part) {
@@ -224,12 +235,12 @@ __global__ void __launch_bounds__(kAThreads, 1)
             mbar_init(bar(kABVClean + s), 2);
             mbar_init(bar(kABVGo + s), 1);
         }
-        for (int i = 0; i < 4; ++i) {
-            mbar_init(bar(kABS + i), 1);
-            mbar_init(bar(kABP + i), 4);
+        for (int h = 0; h < 2; ++h) {
+            mbar_init(bar(kABS + h), 1);
+            mbar_init(bar(kABL + h), 4);
+            mbar_init(bar(kABP + h), 4);
+            mbar_init(bar(kABO + h), 1);
         }
-        mbar_init(bar(kABO), 1);
-        mbar_init(bar(kABO + 1), 1);
         mbar_init(bar(kABDrain), 1);
         *abort = 0;
         *repaired = 0;
@@ -243,13 +254,15 @@ __global__ void __launch_bounds__(kAThreads, 1)
     bool bad_page = false;
     const uint8_t* pages_ok = a.pages_ok ? a.pages_ok + (size_t)b * (a.kv_pad / kAN) + j0 : nullptr;
     if (pages_ok)
-        for (int j = threadIdx.x; j < nt; j += kAThreads) bad_page |= pages_ok[j] != 0xff;
+        for (int j = threadIdx.x; j < n; j += kAThreads) bad_page |= pages_ok[j] != 0xff;
     tc_fence_before();
     bad_page = __syncthreads_or(bad_page);
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
-    // columns: half 0's score buffers (64 each, P over a buffer's first 32) | half 1's | O0 | O1
+    constexpr uint32_t kColP = 128, kColO = 256;  // columns: scores | P0 | P1 (64 each) | O0 | O1 (128 each)
 
+    if (warp >= 8) {
+        set_registers_down<kAOtherRegs>();
     if (warp == 9) {
         // ------------------------------------------------------------ producer
         if (lane == 0) {
@@ -273,8 +286,8 @@ __global__ void __launch_bounds__(kAThreads, 1)
             };
             bool ok = load(&tk_map, kABKFull, kABKEmpty, kAOffK, kAKStages, 0);
             kj = ok;
-            for (int j = 0; ok && j < nt; ++j) {
-                if (j + 1 < nt) {
+            for (int j = 0; ok && j < n; ++j) {
+                if (j + 1 < n) {
                     ok = load(&tk_map, kABKFull, kABKEmpty, kAOffK, kAKStages, j + 1);
                     kj += ok;
                 }
@@ -296,7 +309,7 @@ __global__ void __launch_bounds__(kAThreads, 1)
     } else if (warp == 8) {
         // ------------------------------------------------------------ MMA issuer
         // (the whole warp, converged: see umma_ss_warp; all 512 columns are ours, from 0 on)
-        constexpr uint32_t id_s = idesc_f16(128, kAS), id_o = idesc_f16(128, kDim) | (1u << 16);
+        constexpr uint32_t id_s = idesc_f16(128, kAN), id_o = idesc_f16(128, kDim) | (1u << 16);
         const uint32_t q_lo = sw128_desc_lo(sbase + kAOffQ), k_lo = sw128_desc_lo(sbase + kAOffK);
         const uint32_t v_lo = v_desc_lo(sbase + kAOffV);
         auto wait = [&](int i, uint32_t parity) -> bool {
@@ -304,23 +317,23 @@ __global__ void __launch_bounds__(kAThreads, 1)
             if (lane == 0) give_up();
             return false;
         };
-        // scores of half h into its buffer u: the u-th 64 keys of the tile in `stage`
-        auto scores = [&](int h, int u, int stage) {
-            const uint32_t ql = q_lo + h * (kATile >> 4), kl = k_lo + stage * (kATile >> 4) + u * (kAS * 128 >> 4);
+        const uint32_t lead = elect_lane();
+        auto scores = [&](int h, int stage) {
+            const uint32_t ql = q_lo + h * (kATile >> 4), kl = k_lo + stage * (kATile >> 4);
 #pragma unroll
             for (int ks = 0; ks < 8; ++ks) {
                 const uint32_t o = (uint32_t)(ks & 3) * 2 + (uint32_t)(ks >> 2) * (kAHalf >> 4);
-                umma_ss_warp(h * 128 + u * kAS, sw128_desc(ql + o), sw128_desc(kl + o), id_s, ks > 0);
+                umma_ss_warp(lead, 0, sw128_desc(ql + o), sw128_desc(kl + o), id_s, ks > 0);
             }
-            umma_commit_warp(bar(kABS + 2 * h + u));
+            umma_commit_warp(lead, bar(kABS + h));
         };
-        auto values = [&](int h, int u, int stage, bool first) {
-            const uint32_t vl = v_lo + stage * (kATile >> 4) + u * (kAS * 128 >> 4);
+        auto values = [&](int h, int stage, bool first) {
+            const uint32_t vl = v_lo + stage * (kATile >> 4);
 #pragma unroll
-            for (int ks = 0; ks < 4; ++ks)
-                umma_ts_warp(256 + h * 128, h * 128 + u * kAS + ks * 8, sw128_desc(vl + ks * (2048 >> 4)), id_o,
+            for (int ks = 0; ks < 8; ++ks)
+                umma_ts_warp(lead, kColO + h * 128, kColP + h * 64 + ks * 8, sw128_desc(vl + ks * (2048 >> 4)), id_o,
                              !(first && ks == 0));
-            umma_commit_warp(bar(kABO + h));
+            umma_commit_warp(lead, bar(kABO + h));
         };
         bool ok = tmem == 0;
         if (!ok && lane == 0) {
@@ -328,57 +341,61 @@ __global__ void __launch_bounds__(kAThreads, 1)
             atomicOr(a.err, TQ_DEVERR_INTERNAL);
         }
         ok = ok && wait(kABQ, 0) && wait(kABKFull, 0);
-        if (ok) {
+        int user = -1;               // whose scores the buffer last held, and of which tile
+        uint32_t used = 0;
+        auto next_scores = [&](int h, int j, int stage) {
+            if (ok && user >= 0) ok = wait(kABL + user, used);
+            if (!ok) return;
             tc_fence_after();
-#pragma unroll
-            for (int u = 0; u < 2; ++u)
-#pragma unroll
-                for (int h = 0; h < 2; ++h)
-                    if (u < (h ? n1 : n0)) scores(h, u, 0);
-            umma_commit_warp(bar(kABKEmpty));
-        }
+            scores(h, stage);
+            user = h;
+            used = (uint32_t)j;
+        };
+        if (n0) next_scores(0, 0, 0);
+        if (n1) next_scores(1, 0, 0);
+        if (ok) umma_commit_warp(lead, bar(kABKEmpty));
         int vs = 0, kn = 0;          // stages of tile j's values and of tile j + 1's keys
         uint32_t vp = 0, kp = 0;     // and their phases
-        for (int j = 0; ok && j < nt; ++j) {
+        for (int j = 0; ok && j < n; ++j) {
             if (++kn == kAKStages) {
                 kn = 0;
                 kp ^= 1u;
             }
-            ok = j >= masked_from ? wait(kABVClean + vs, (j - masked_from) / kAVStages) : wait(kABVFull + vs, vp);
-            if (ok && j + 1 < nt) ok = wait(kABKFull + kn, kp);
+            if (j + 1 < n) ok = wait(kABKFull + kn, kp);
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const int nh = h ? n1 : n0, i = 2 * j + u;
-                    if (!ok || i >= nh) continue;
-                    ok = wait(kABP + 2 * h + u, j);
-                    if (!ok) continue;
-                    tc_fence_after();
-                    values(h, u, vs, i == 0);
-                    if (i + 2 < nh) scores(h, u, kn);
+            for (int h = 0; h < 2; ++h) {
+                const int nh = h ? n1 : n0;
+                if (j + 1 < nh) next_scores(h, j + 1, kn);
+                if (ok && h == 0)
+                    ok = j >= masked_from ? wait(kABVClean + vs, (j - masked_from) / kAVStages) : wait(kABVFull + vs, vp);
+                if (ok && j < nh) {
+                    ok = wait(kABP + h, j);
+                    if (ok) {
+                        tc_fence_after();
+                        values(h, vs, j == 0);
+                    }
                 }
             }
             if (!ok) break;
-            umma_commit_warp(bar(kABVEmpty + vs));
-            if (j + 1 < nt) umma_commit_warp(bar(kABKEmpty + kn));
+            umma_commit_warp(lead, bar(kABVEmpty + vs));
+            if (j + 1 < n) umma_commit_warp(lead, bar(kABKEmpty + kn));
             if (++vs == kAVStages) {
                 vs = 0;
                 vp ^= 1u;
             }
         }
         // nothing is in flight when the CTA exits
-        umma_commit_warp(bar(kABDrain));
+        umma_commit_warp(lead, bar(kABDrain));
         const volatile int never = 0;
         mbar_wait(bar(kABDrain), 0, &never, kAWaitNs);
         __syncwarp();
-    } else if (warp >= 10) {
+    } else {
         // ------------------------------------------------------------ masked tiles' values
-        for (int j = masked_from; j < nt; ++j) {
+        for (int j = masked_from; j < n; ++j) {
             const int s = j % kAVStages;
             // (these warps do not follow the unmasked tiles' phases of the stage: its load's
             // issue tells them that the phase of this tile is the current one)
-            if (!mbar_wait_warp(bar(kABVGo + s), (uint32_t)((j - masked_from) / kAVStages) & 1u, abort, kAWaitNs) ||
+            if (!__all_sync(0xffffffffu, mbar_wait_asleep(bar(kABVGo + s), (uint32_t)((j - masked_from) / kAVStages) & 1u, abort, kAWaitNs)) ||
                 !mbar_wait_warp(bar(kABVFull + s), (uint32_t)(j / kAVStages) & 1u, abort, kAWaitNs)) {
                 give_up();
                 break;
@@ -409,16 +426,19 @@ __global__ void __launch_bounds__(kAThreads, 1)
             fence_proxy_async_shared();
             mbar_arrive_warp(bar(kABVClean + s));
         }
+    }
     } else {
+        set_registers_up<kASoftmaxRegs>();
         // ------------------------------------------------------------ softmax
         const int h = warp >> 2, row = threadIdx.x & 127;
         const int nh = h ? n1 : n0;
         const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // this warp's 32 lanes
-        const uint32_t ts = tmem + h * 128 + lanes, to = tmem + 256 + h * 128 + lanes;
+        const uint32_t ts = tmem + lanes, tp = tmem + kColP + h * 64 + lanes, to = tmem + kColO + h * 128 + lanes;
         const int qi = q0 + h * a.QT + row / a.G;           // this row's query
         const bool live = row < a.G * a.QT && qi < nq;
         const int limit = live ? off + qi - j0 * kAN : -1;  // its last token
-        const int half_masked = (off + q0 + h * a.QT + 1) / kAS - 2 * j0;  // first step with a masked pair
+        const int half_masked = (off + q0 + h * a.QT + 1) / kAN - j0;  // first tile with a masked pair
+        const uint32_t lead = lane == 0;
         const float2 sc = make_float2(a.scale_log2, a.scale_log2);
         float m = -INFINITY;
         float2 sum[2] = {{0.f, 0.f}, {0.f, 0.f}};
@@ -428,27 +448,28 @@ __global__ void __launch_bounds__(kAThreads, 1)
             give_up();
             return false;
         };
-        for (int i = 0; i < nh; ++i) {
-            const uint32_t tb = ts + (i & 1) * kAS;
-            ok = wait(kABS + 2 * h + (i & 1), i / 2);
+        for (int j = 0; j < nh; ++j) {
+            ok = wait(kABS + h, j);
             if (!ok) break;
             tc_fence_after();
-            uint32_t s[2][32];
-            tmem_ld32(tb, s[0]);
-            tmem_ld32(tb + 32, s[1]);
-            tmem_ld_wait();
-            if (i >= half_masked) {
-                const int lim = limit - i * kAS;
+            uint32_t s[4][32];
 #pragma unroll
-                for (int q = 0; q < 2; ++q)
+            for (int q = 0; q < 4; ++q) tmem_ld32(ts + 32 * q, s[q]);
+            tmem_ld_wait();
+            tc_fence_before();
+            mbar_arrive_lead(lead, bar(kABL + h));
+            if (j >= half_masked) {
+                const int lim = limit - j * kAN;
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
 #pragma unroll
                     for (int e = 0; e < 32; ++e)
                         if (32 * q + e > lim) s[q][e] = 0xFF800000u;  // -inf
             }
             if (bad_page) {
-                const int okp = pages_ok[i / 2] >> (4 * (i & 1));
+                const int okp = pages_ok[j];
 #pragma unroll
-                for (int q = 0; q < 2; ++q)
+                for (int q = 0; q < 4; ++q)
 #pragma unroll
                     for (int e = 0; e < 32; ++e)
                         if (!((okp >> (2 * q + e / 16)) & 1)) s[q][e] = 0xFF800000u;
@@ -456,24 +477,26 @@ __global__ void __launch_bounds__(kAThreads, 1)
             float mx[4];
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-                const uint32_t* x = &s[q / 2][16 * (q & 1)];
-                mx[q] = max3(__uint_as_float(x[0]), __uint_as_float(x[1]), __uint_as_float(x[2]));
+                mx[q] = max3(__uint_as_float(s[q][0]), __uint_as_float(s[q][1]), __uint_as_float(s[q][2]));
 #pragma unroll
-                for (int e = 3; e < 15; e += 2) mx[q] = max3(mx[q], __uint_as_float(x[e]), __uint_as_float(x[e + 1]));
-                mx[q] = fmaxf(mx[q], __uint_as_float(x[15]));
+                for (int e = 3; e < 31; e += 2) mx[q] = max3(mx[q], __uint_as_float(s[q][e]), __uint_as_float(s[q][e + 1]));
+                mx[q] = max3(mx[q], mx[q], __uint_as_float(s[q][31]));
             }
-            const float top = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * a.scale_log2;
-            const bool grow = top > m + kRescale || (m == -INFINITY && top > m);
+            float top = max3(max3(mx[0], mx[1], mx[2]), mx[3], mx[3]) * a.scale_log2;
+            // a NaN or infinite score makes the row's sum and outputs NaN; the maximum carries it
+            if (!(top < INFINITY)) top = NAN;
+            const bool grow = top > m + kRescale || (m == -INFINITY && top > m) || (top != top && m == m);
+            // the tile before is in O, and its P has been read
+            if (j > 0) ok = wait(kABO + h, j - 1);
+            if (!ok) break;
             if (__any_sync(0xffffffffu, grow)) {
                 const float mn = grow ? top : m;
-                if (i > 0) {
+                if (j > 0) {
                     const float f = grow ? ex2(m - mn) : 1.f;  // (first maximum: ex2(-inf) = 0)
 #pragma unroll
                     for (int q = 0; q < 2; ++q) sum[q] = __fmul2_rn(sum[q], make_float2(f, f));
-                    ok = wait(kABO + h, i - 1);  // the step before is in O
-                    if (!ok) break;
                     tc_fence_after();
-#pragma unroll
+#pragma unroll 1
                     for (int q = 0; q < 8; ++q) {
                         uint32_t o[16];
                         tmem_ld16(to + 16 * q, o);
@@ -492,24 +515,26 @@ __global__ void __launch_bounds__(kAThreads, 1)
             }
             const float mm = m == -INFINITY ? 0.f : m;
             const float2 nm = make_float2(-mm, -mm);
-            uint32_t p[32];
 #pragma unroll
-            for (int e = 0; e < 32; ++e) {
-                float2 x = make_float2(__uint_as_float(s[e / 16][2 * e % 32]), __uint_as_float(s[e / 16][2 * e % 32 + 1]));
-                x = __ffma2_rn(x, sc, nm);
-                x.x = ex2(x.x);
-                x.y = ex2(x.y);
-                sum[e & 1] = __fadd2_rn(sum[e & 1], x);
-                const __half2 hp = __floats2half2_rn(x.x, x.y);
-                p[e] = *reinterpret_cast<const uint32_t*>(&hp);
+            for (int q = 0; q < 2; ++q) {
+                uint32_t p[32];
+#pragma unroll
+                for (int e = 0; e < 32; ++e) {
+                    float2 x = make_float2(__uint_as_float(s[2 * q + e / 16][2 * e % 32]),
+                                           __uint_as_float(s[2 * q + e / 16][2 * e % 32 + 1]));
+                    x = __ffma2_rn(x, sc, nm);
+                    x.x = ex2(x.x);
+                    x.y = ex2(x.y);
+                    sum[e & 1] = __fadd2_rn(sum[e & 1], x);
+                    const __half2 hp = __floats2half2_rn(x.x, x.y);
+                    p[e] = *reinterpret_cast<const uint32_t*>(&hp);
+                }
+                tmem_st32(tp + 32 * q, p);
             }
-            tmem_st32(tb, p);
             tmem_st_wait();
             tc_fence_before();
-            mbar_arrive_warp(bar(kABP + 2 * h + (i & 1)));
+            mbar_arrive_lead(lead, bar(kABP + h));
         }
-        // the last two steps' sums, in order (the scores of step i say that step i - 2 is in O)
-        if (ok && nh > 1) ok = wait(kABO + h, nh - 2);
         if (ok && nh > 0) ok = wait(kABO + h, nh - 1);
         const float l = (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
         const size_t orow = (size_t)(c0 + qi) * a.Hq + (a.head0 + hk) * a.G + row % a.G;
@@ -597,7 +622,11 @@ cudaError_t launch_attend(const tq_ctx* ctx, const AttendCall& c, cudaStream_t s
         !encode_heads_tmap(&mk, c.k, c.heads, kv_rows, c.k_stride, 1, kAN) ||
         !encode_heads_tmap(&mv, c.v, c.heads, kv_rows, c.v_stride, 1, kAN))
         return cudaErrorInvalidValue;
-    cudaError_t e = cudaFuncSetAttribute(attend_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kASmem);
+    cudaFuncAttributes attr{};
+    cudaError_t e = cudaFuncGetAttributes(&attr, attend_tc_kernel);
+    if (e != cudaSuccess) return e;
+    if (attr.numRegs != kARegs) return cudaErrorInvalidConfiguration;  // the register split would not add up
+    e = cudaFuncSetAttribute(attend_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kASmem);
     if (e != cudaSuccess) return e;
     // slots of all sequences: floor(total / q) + B bounds every sequence's last one
     const long long slots = (long long)c.total_q / (2 * a.QT) + c.B;

@@ -223,6 +223,7 @@ __global__ void __launch_bounds__(kUThreads, 1)
         const uint32_t S = (((sbase + kUOffS) >> 4) & 0x3FFFu) | ((kUHalf >> 4) << 16);
         long long i = blockIdx.x;
         Item it;
+        const uint32_t lead = elect_lane();
         bool ok = tmem == 0;
         if (!ok && lane == 0) {
             *abort = 1;
@@ -238,12 +239,12 @@ __global__ void __launch_bounds__(kUThreads, 1)
 #pragma unroll
             for (int ks = 0; ks < 8; ++ks) {
                 const uint32_t o = (uint32_t)(ks & 3) * 2 + (uint32_t)(ks >> 2) * (kUHalf >> 4);
-                umma_ss_warp(0, sw128_desc(A + o), sw128_desc(R + o), id_k, ks > 0);
+                umma_ss_warp(lead, 0, sw128_desc(A + o), sw128_desc(R + o), id_k, ks > 0);
                 if (PROD)
-                    umma_ss_warp(128, sw128_desc(A + (kUTile >> 4) + o), sw128_desc(S + ks * (2048 >> 4)), id_n, ks > 0);
-                umma_ss_warp(256, sw128_desc(A + 2 * (kUTile >> 4) + o), sw128_desc(R + o), id_k, ks > 0);
+                    umma_ss_warp(lead, 128, sw128_desc(A + (kUTile >> 4) + o), sw128_desc(S + ks * (2048 >> 4)), id_n, ks > 0);
+                umma_ss_warp(lead, 256, sw128_desc(A + 2 * (kUTile >> 4) + o), sw128_desc(R + o), id_k, ks > 0);
             }
-            umma_commit_warp(bar(kUBD));
+            umma_commit_warp(lead, bar(kUBD));
         }
         // the operand matrices have landed and no MMA is in flight when the CTA exits
         const volatile int never = 0;

@@ -256,34 +256,60 @@ __device__ __forceinline__ void umma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64
         "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
         : "memory");
 }
-// The same two from a converged warp, one of whose lanes issues.  Every lane computes the
-// operands, so they stay in uniform registers: an MMA issued under `if (lane == 0)` moves
-// each of them there first and held the thread about 105 cycles among busy warps, more than
-// the 65 that the MMA itself takes.
-__device__ __forceinline__ void umma_ss_warp(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
-                                             uint32_t accumulate) {
+// The same two from a converged warp, of which the lane with `lead` set issues.  Every lane
+// computes the operands, so they stay in uniform registers: an MMA issued under
+// `if (lane == 0)` moves each of them there first and held the thread about 105 cycles among
+// busy warps, more than the 65 that the MMA itself takes.  (An elect.sync per MMA costs about
+// 95 cycles; the lane is chosen once.)
+__device__ __forceinline__ uint32_t elect_lane() {
+    uint32_t e;
+    asm volatile("{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\tselp.u32 %0, 1, 0, e;\n\t}" : "=r"(e));
+    return e;
+}
+__device__ __forceinline__ void umma_ss_warp(uint32_t lead, uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                             uint32_t idesc, uint32_t accumulate) {
     asm volatile(
-        "{\n\t.reg .pred p, e;\n\telect.sync _|e, 0xffffffff;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "{\n\t.reg .pred p, e;\n\tsetp.ne.b32 e, %5, 0;\n\tsetp.ne.b32 p, %4, 0;\n\t"
         "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(lead)
         : "memory");
 }
-__device__ __forceinline__ void umma_ts_warp(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc,
-                                             uint32_t accumulate) {
+__device__ __forceinline__ void umma_ts_warp(uint32_t lead, uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
+                                             uint32_t idesc, uint32_t accumulate) {
     asm volatile(
-        "{\n\t.reg .pred p, e;\n\telect.sync _|e, 0xffffffff;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "{\n\t.reg .pred p, e;\n\tsetp.ne.b32 e, %5, 0;\n\tsetp.ne.b32 p, %4, 0;\n\t"
         "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(lead)
         : "memory");
 }
-// Arrive once on `bar` when every MMA the warp has issued so far has completed.
-__device__ __forceinline__ void umma_commit_warp(uint32_t bar) {
+// Arrive once on `bar` when every MMA that lane has issued so far has completed.
+__device__ __forceinline__ void umma_commit_warp(uint32_t lead, uint32_t bar) {
     asm volatile(
-        "{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\t"
-        "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar)
+        "{\n\t.reg .pred e;\n\tsetp.ne.b32 e, %1, 0;\n\t"
+        "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar), "r"(lead)
         : "memory");
 }
-// A wait of every lane, with one answer for the warp.
+// mbar_arrive_warp by the lane with `lead` set, without a branch.
+__device__ __forceinline__ void mbar_arrive_lead(uint32_t lead, uint32_t bar) {
+    __syncwarp();
+    asm volatile("{\n\t.reg .pred e;\n\tsetp.ne.b32 e, %1, 0;\n\t@e mbarrier.arrive.shared::cta.b64 _, [%0];\n\t}" ::"r"(bar),
+                 "r"(lead)
+                 : "memory");
+}
+// mbar_wait for a thread that has long to wait and nothing to be late for: it sleeps between
+// tests, which otherwise take issue slots from the warps beside it.
+__device__ __forceinline__ bool mbar_wait_asleep(uint32_t bar, uint32_t parity, const volatile int* abort,
+                                                 uint64_t limit_ns) {
+    const uint64_t t0 = globaltimer_ns();
+    while (!mbar_try_wait(bar, parity)) {
+        if (*abort || globaltimer_ns() - t0 > limit_ns) return false;
+        __nanosleep(500);
+    }
+    return true;
+}
+// mbar_wait by every lane, with one answer for the warp.  (The clock it reads after a failed
+// test is also what keeps it from testing all the time: with 64 tests first, the attention
+// kernel's period grew from 3180 to 3720 cycles.)
 __device__ __forceinline__ bool mbar_wait_all(uint32_t bar, uint32_t parity, const volatile int* abort,
                                               uint64_t limit_ns) {
     return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort, limit_ns)) != 0;
