@@ -83,34 +83,6 @@ __device__ __forceinline__ float max3(float x, float y, float z) {
     return m;
 }
 
-template <int N>
-__device__ __forceinline__ void set_registers_up() {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
-}
-template <int N>
-__device__ __forceinline__ void set_registers_down() {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
-}
-
-__device__ __forceinline__ void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
-        "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
-        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
-        "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
-        "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
-        : "memory");
-}
-
-__device__ __forceinline__ void tma_load_3d(uint32_t dst, const void* tmap, int x, int y, int z, uint32_t bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], "
-        "[%5];" ::"r"(dst),
-        "l"(tmap), "r"(x), "r"(y), "r"(z), "r"(bar)
-        : "memory");
-}
-
 // V as the B operand: [token][64 coordinates] rows of 128 bytes, 128-byte swizzle, the
 // coordinates (N) contiguous.  LBO: from one 64-coordinate block to the next; SBO: from
 // one 8-token group to the next.
@@ -136,22 +108,6 @@ struct Args {
     uint32_t* err;
 };
 
-// Sequence of tile slot s: the last b with floor(cu[b] / q) + b <= s.  (Sequence b's
-// ceil(n_b / q) tiles fit its slots: floor((c + n) / q) + 1 >= floor(c / q) + ceil(n / q).)
-// All 32 lanes probe at once.
-__device__ __forceinline__ int find_seq(const int32_t* cu, int B, int q, int s, int lane) {
-    int lo = 0, n = B;  // the answer is in [lo, lo + n)
-    while (n > 1) {
-        const int step = (n + 31) / 32;
-        const int b = lo + lane * step;
-        const bool ok = lane * step < n && (lane == 0 || cu[b] / q + b <= s);
-        const int last = 31 - __clz(__ballot_sync(0xffffffffu, ok));
-        lo += last * step;
-        n = min(step, n - last * step);
-    }
-    return lo;
-}
-
 __global__ void __launch_bounds__(kAThreads, 1)
     attend_tc_kernel(const __grid_constant__ CUtensorMap tq_map, const __grid_constant__ CUtensorMap tk_map,
                      const __grid_constant__ CUtensorMap tv_map, const Args a) {
@@ -170,7 +126,7 @@ __global__ void __launch_bounds__(kAThreads, 1)
             if (a.cu_q[b] < 0 || a.cu_q[b + 1] < a.cu_q[b] || a.cu_q[b + 1] > a.total_q)
                 atomicOr(a.err, TQ_DEVERR_SEQLEN);
     }
-    const int b = find_seq(a.cu_q, a.B, QC, slot, lane);
+    const int b = find_tile_seq(a.cu_q, a.B, QC, slot, lane);
     const int c0 = a.cu_q[b], nq = a.cu_q[b + 1] - c0;
     if (c0 < 0 || nq <= 0 || c0 + nq > a.total_q) return;
     const int tiles = (nq + QC - 1) / QC;

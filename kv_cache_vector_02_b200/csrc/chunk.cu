@@ -40,6 +40,8 @@ constexpr uint32_t kUOffBar = kUOffOut + 2 * kUTile;
 constexpr uint32_t kUSmem = kUOffBar + 256;
 static_assert(kUSmem <= 232448, "shared memory budget");
 constexpr uint64_t kUWaitNs = 2000000000ull;
+// At most so many (query, head of a group) rows a sequence on average: chunk_few.cu.
+constexpr int kFewRows = 128;
 constexpr size_t kDecompressedMost = size_t(1) << 30;   // keys and values decompressed at a time
 
 enum : int { kUBConst = 0, kUBA = 1, kUBD = 2, kUBDEmpty = 3, kUNumBars = 4 };
@@ -363,15 +365,7 @@ __global__ void __launch_bounds__(256) chunk_combine_kernel(const CombineArgs a)
     const int lane = threadIdx.x & 31;
     if (w >= (long long)a.total_q * a.cols) return;
     const int qi = (int)(w / a.cols), h = a.col0 + (int)(w - (long long)qi * a.cols);
-    // the row's sequence: the last one that begins at or before it
-    int lo = 0, n = a.B;
-    while (n > 1) {
-        const int step = (n + 31) / 32;
-        const bool le = lane * step < n && (lane == 0 || a.cu_q[lo + lane * step] <= qi);
-        const int last = 31 - __clz(__ballot_sync(0xffffffffu, le));
-        lo += last * step;
-        n = min(step, n - last * step);
-    }
+    const int lo = find_row_seq(a.cu_q, a.B, qi, lane);
     const int c0 = a.cu_q[lo], c1 = a.cu_q[lo + 1], len = a.seq_lens[lo];
     if (qi < c0 || qi >= c1 || c0 < 0 || c1 > a.total_q || len < c1 - c0 || len > a.max_kv) return;
     const size_t rows = (size_t)a.total_q * a.Hq, row = (size_t)qi * a.Hq + h;
@@ -425,25 +419,26 @@ size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
 
 ChunkPlan plan_chunk(const tq_ctx* ctx, int B, int total_q, int Hq, int Hkv, int max_seq_len) {
     ChunkPlan p{};
+    p.few = (long long)total_q * (Hq / Hkv) <= (long long)kFewRows * B;
     const long long tiles = max_seq_len > 0 ? ((long long)max_seq_len + 127) / 128 : 1;
     const long long rows = (long long)B * tiles * 128;
     if (rows > 0x7FFFFFFFll) return p;  // TMA coordinates are 32-bit
     p.kv_pad = (int)(tiles * 128);
     const size_t head_bytes = (size_t)rows * kDim * 2 * 2;
     p.heads = Hkv;
-    if (head_bytes * Hkv > kDecompressedMost) {
+    if (!p.few && head_bytes * Hkv > kDecompressedMost) {
         p.heads = (int)(kDecompressedMost / (head_bytes ? head_bytes : 1));
         if (p.heads < 1) p.heads = 1;
     }
     // Splits of the tokens: as many as make the waves over the SMs shortest, each split
     // costing about three tiles more (its start and end, and its part of the join).
-    const int G = Hq / Hkv, QC = 2 * (128 / G);
+    const int G = Hq / Hkv, QC = (p.few ? 1 : 2) * (128 / G);
     long long ctas = (total_q + QC - 1) / QC;
     if (ctas < B) ctas = B;
     ctas *= p.heads;
     p.splits = 1;
     double best = 0.;
-    for (int s = 1; s <= 32 && (s == 1 || tiles >= 4 * s); ++s) {
+    for (int s = 1; s <= 32 && (s == 1 || tiles >= (p.few ? 2 : 4) * s); ++s) {
         const double waves = double((ctas * s + ctx->sm_count - 1) / ctx->sm_count);
         const double cost = waves * (double(tiles) / s + 3.) + (s > 1 ? 2. : 0.);
         if (s == 1 || cost < best) {
@@ -457,6 +452,13 @@ ChunkPlan plan_chunk(const tq_ctx* ctx, int B, int total_q, int Hq, int Hkv, int
         off = up256(off + n);
         return at;
     };
+    if (p.few) {
+        p.k_off = take((size_t)total_q * Hq * 2 * kDim * 2);  // the rotated queries
+        p.part_off = take((size_t)p.splits * total_q * Hq * kDim * 4);
+        p.ml_off = take((size_t)p.splits * total_q * Hq * 8);
+        p.bytes = off + 256;
+        return p;
+    }
     p.k_off = take(head_bytes / 2 * p.heads);
     p.v_off = take(head_bytes / 2 * p.heads);
     p.pages_off = take((size_t)B * tiles);
@@ -469,6 +471,7 @@ ChunkPlan plan_chunk(const tq_ctx* ctx, int B, int total_q, int Hq, int Hkv, int
 }
 
 cudaError_t launch_chunk(const tq_ctx* ctx, const ChunkPlan& plan, const ChunkCall& c, cudaStream_t stream) {
+    if (plan.few) return launch_chunk_few(ctx, plan, c, stream);
     uint8_t* ws = c.workspace;
     uint16_t* k = reinterpret_cast<uint16_t*>(ws + plan.k_off);
     uint16_t* v = reinterpret_cast<uint16_t*>(ws + plan.v_off);

@@ -1,0 +1,758 @@
+// Attention of few new tokens over the paged compressed cache: the way of tq_chunk_attention
+// for verification, short follow-ups and single tokens, where decompressing the pages first
+// would cost more than the attention.  Everything happens in the rotated domain, as in the
+// decode, on tcgen05 with the packed pages read once:
+//   s_t = a_t <q', c_k> + b_t <s, sigma>,  q' = R^T q, s = S q,
+//         a_t = scale n_t / sqrt(d),  b_t = scale gamma_t sqrt(pi/2) / d,
+//   acc = sum_t p_t (n_t / sqrt(d)) c_v,   o = R acc / sum_t p_t.
+//
+// few_rotate_kernel   q' and s of every (query, head), fp16 (R^T as fp16 hi + lo)
+// few_attend_kernel   one CTA per (128 rows, kv head, split of the tokens); a row is a
+//                     (query, query head of the group) pair.  Per tile of 128 tokens:
+//   warps 4-11  two threads per token: its packed codes and signs (loaded a tile ahead)
+//               become fp16 levels and +-1 in registers, the values' times n_t/sqrt(d)
+//               (rounded to fp16, as decompressed values are), and go to swizzled
+//               operand tiles; a_t, b_t to shared memory
+//   warp 12     D1 = Q' C_k^T, D2 = S_q Sigma^T, O += P V on tcgen05
+//   warps 0-3   one thread per row: s = a_t D1 + b_t D2 (fp32; the score's two scalars are
+//               never rounded), mask, running maximum and sum, P to tensor memory.  Warps
+//               without a row only keep step.
+// few_join_kernel     the splits joined, o = R acc / l in fp32
+//
+// A tile takes 24 MMAs of 65 cycles (16 without signs) whatever the rows, which is what bounds
+// it: 1560 cycles for 20 KB of pages.
+#include <cmath>
+
+#include <cuda.h>
+
+#include "dequant.cuh"
+#include "device_util.cuh"
+#include "mma_sync.cuh"
+#include "sm100.cuh"
+
+namespace tq {
+namespace {
+
+using namespace sm100;
+
+constexpr int kFN = 128;                            // tokens of a tile
+constexpr uint32_t kFTile = 128 * kDim * 2, kFHalf = kFTile / 2;
+constexpr int kFThreads = 512;
+// Registers: 128 a thread at launch (the launch checks it), moved to the softmax.
+constexpr int kFRegs = 128, kFSoftmaxRegs = 208, kFCodeRegs = 112, kFIssueRegs = 80;
+static_assert(kFSoftmaxRegs + 2 * kFCodeRegs + kFIssueRegs == 4 * kFRegs, "the block's own registers");
+constexpr uint32_t kFOffQ = 0;                      // q' | s, 128 rows each
+constexpr uint32_t kFOffK = 2 * kFTile;             // two buffers of C_k | Sigma
+constexpr uint32_t kFOffV = kFOffK + 4 * kFTile;    // C_v n / sqrt(d)
+constexpr uint32_t kFOffScal = kFOffV + kFTile;     // float2 [2][128]: a_t, b_t
+constexpr uint32_t kFOffBar = kFOffScal + 2 * 128 * 8;
+constexpr uint32_t kFSmem = kFOffBar + 256;
+static_assert(kFSmem <= 232448, "shared memory budget");
+constexpr uint64_t kFWaitNs = 2000000000ull;
+constexpr float kFRescale = 8.f;  // log2 of what P may grow to before O is rescaled
+constexpr uint32_t kFColS2 = 128, kFColO = 256, kFColP = 384;
+
+enum : int {
+    kFBQ = 0,
+    kFBKFull = 1,   // +buffer
+    kFBKEmpty = 3,  // +buffer
+    kFBVFull = 5,
+    kFBO = 6,       // a tile's P V added (and its values read)
+    kFBS = 7,       // scores in tensor memory
+    kFBL = 8,       // scores in registers
+    kFBP = 9,       // P in tensor memory
+    kFBDrain = 10,
+    kFNumBars = 11
+};
+
+struct FewArgs {
+    const uint8_t* kc;
+    const uint8_t* vc;
+    int num_blocks;
+    const int32_t* block_table;
+    int max_blocks;
+    const int32_t* cu_q;
+    const int32_t* seq_lens;
+    int B, total_q, max_kv;
+    int Hq, Hkv, G, QT;      // QT = 128 / G queries per CTA
+    ChunkLayout lk, lv;
+    LevelTable tk, tv;
+    float qscale, sscale;    // scale log2(e) / sqrt(d), scale log2(e) sqrt(pi/2) / d
+    float vscale;            // 1 / sqrt(d)
+    float* part;             // [splits][total_q * Hq][128] unscaled sums, rotated
+    float2* ml;              // [splits][total_q * Hq] maximum (base 2) and sum
+    void* out;               // rows of sequences with impossible lengths are zeroed here
+    int out_fp32;
+    uint32_t* err;
+};
+
+__device__ __forceinline__ float few_ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+// The largest of three; NaN if one is.
+__device__ __forceinline__ float few_max3(float x, float y, float z) {
+    float m;
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(m) : "f"(x), "f"(y), "f"(z));
+    return m;
+}
+
+// Half a row of packed codes of W bits: 8 W bytes.
+template <int W>
+struct HalfRow {
+    uint32_t w[2 * W];
+    __device__ __forceinline__ void load(const uint8_t* p) {
+        if (W == 4) {
+#pragma unroll
+            for (int i = 0; i < W / 2; ++i) {
+                const uint4 x = *reinterpret_cast<const uint4*>(p + 16 * i);
+                w[4 * i] = x.x;
+                w[4 * i + 1] = x.y;
+                w[4 * i + 2] = x.z;
+                w[4 * i + 3] = x.w;
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < W; ++i) {
+                const uint2 x = *reinterpret_cast<const uint2*>(p + 8 * i);
+                w[2 * i] = x.x;
+                w[2 * i + 1] = x.y;
+            }
+        }
+    }
+    // the codes of the half's coordinates 8c .. 8c + 7
+    __device__ __forceinline__ uint32_t codes(int c) const { return w[8 * W * c / 32] >> (8 * W * c % 32); }
+};
+
+template <int WK, int LK, bool PROD, int WV, int LV>
+__global__ void __launch_bounds__(kFThreads, 1)
+    few_attend_kernel(const __grid_constant__ CUtensorMap q_map, const FewArgs a) {
+    extern __shared__ __align__(1024) uint8_t smem[];
+    const uint32_t sbase = smem_u32(smem);
+    const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+    if (sbase & 1023u) {
+        if (threadIdx.x == 0) atomicOr(a.err, TQ_DEVERR_INTERNAL);
+        return;
+    }
+    const int slot = (int)(blockIdx.x / (unsigned)a.Hkv), hk = (int)(blockIdx.x % (unsigned)a.Hkv);
+    if (blockIdx.x == 0 && blockIdx.y == 0) {
+        for (int b = threadIdx.x; b < a.B; b += kFThreads)
+            if (a.cu_q[b] < 0 || a.cu_q[b + 1] < a.cu_q[b] || a.cu_q[b + 1] > a.total_q)
+                atomicOr(a.err, TQ_DEVERR_SEQLEN);
+    }
+    const int b = find_tile_seq(a.cu_q, a.B, a.QT, slot, lane);
+    const int c0 = a.cu_q[b], nq = a.cu_q[b + 1] - c0;
+    if (c0 < 0 || nq <= 0 || c0 + nq > a.total_q) return;
+    const int rank = slot - (c0 / a.QT + b);
+    if (rank < 0 || rank >= (nq + a.QT - 1) / a.QT) return;
+    const int q0 = rank * a.QT, nrows = min(a.QT, nq - q0) * a.G;
+    const int kv_len = a.seq_lens[b], off = kv_len - nq;
+    auto out_row = [&](int r) { return (size_t)(c0 + q0 + r / a.G) * a.Hq + hk * a.G + r % a.G; };
+    if (off < 0 || kv_len > a.max_kv) {  // a length that cannot be: zero rows
+        if (blockIdx.y) return;
+        if (threadIdx.x == 0) atomicOr(a.err, TQ_DEVERR_SEQLEN);
+        for (int i = threadIdx.x; i < nrows * kDim; i += kFThreads) {
+            const size_t o = out_row(i / kDim) * kDim + i % kDim;
+            if (a.out_fp32) static_cast<float*>(a.out)[o] = 0.f;
+            else static_cast<__half*>(a.out)[o] = __ushort_as_half(0);
+        }
+        return;
+    }
+    // this split's tiles: j0 .. j0 + n - 1, up to the last query's position
+    const int last = off + min(q0 + a.QT, nq);  // tokens that its last query attends
+    const int all = (last + kFN - 1) / kFN;
+    const int share = (all + (int)gridDim.y - 1) / (int)gridDim.y, j0 = min((int)blockIdx.y * share, all);
+    const int n = min(share, all - j0);
+    const size_t prow0 = (size_t)blockIdx.y * a.total_q * a.Hq;
+    if (n <= 0) {
+        for (int r = threadIdx.x; r < nrows; r += kFThreads) a.ml[prow0 + out_row(r)] = make_float2(-INFINITY, 0.f);
+        return;
+    }
+    const int live_warps = (nrows + 31) / 32;
+
+    const uint32_t bars = sbase + kFOffBar;
+    auto bar = [&](int i) -> uint32_t { return bars + 8u * (uint32_t)i; };
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kFOffBar + 8 * kFNumBars);
+    volatile int* abort = reinterpret_cast<volatile int*>(smem + kFOffBar + 8 * kFNumBars + 4);
+    int* first_bad = reinterpret_cast<int*>(smem + kFOffBar + 8 * kFNumBars + 8);
+    uint8_t* page_bad = smem + kFOffBar + 8 * kFNumBars + 16;  // [2][8]
+    auto give_up = [&] {
+        *abort = 1;
+        atomicOr(a.err, TQ_DEVERR_TIMEOUT);
+    };
+    if (threadIdx.x == 0) {
+        mbar_init(bar(kFBQ), 1);
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(bar(kFBKFull + s), 8);
+            mbar_init(bar(kFBKEmpty + s), (uint32_t)live_warps + 1);  // MMAs done, scalars read
+        }
+        mbar_init(bar(kFBVFull), 8);
+        mbar_init(bar(kFBO), 1);
+        mbar_init(bar(kFBS), 1);
+        mbar_init(bar(kFBL), (uint32_t)live_warps);
+        mbar_init(bar(kFBP), (uint32_t)live_warps);
+        mbar_init(bar(kFBDrain), 1);
+        *abort = 0;
+        *first_bad = 0x7FFFFFFF;
+        fence_mbar_init();
+        const int box = a.G * a.QT * 128;
+        mbar_arrive_expect_tx(bar(kFBQ), (uint32_t)(box * (PROD ? 4 : 2)));
+        for (int x = 0; x < (PROD ? 4 : 2); ++x)
+            tma_load_3d(sbase + kFOffQ + x * kFHalf, &q_map, 64 * x, hk * a.G, c0 + q0, bar(kFBQ));
+    }
+    if (warp == 12) {
+        tmem_alloc(smem_u32(tmem_slot), 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;
+
+    if (warp >= 4 && warp < 12) {
+        set_registers_down<kFCodeRegs>();
+        // ------------------------------------------------------------ codes to operands
+        const int tok = threadIdx.x & 127, half = warp >= 8 ? 1 : 0, r16 = tok % kPage;
+        const uint32_t lead = lane == 0;
+        HalfRow<WK> kw{};
+        HalfRow<WV> vw{};
+        HalfRow<1> sw{};
+        float kn = 0.f, kg = 0.f, vn = 0.f;
+        bool bad = false;
+        auto fetch = [&](int j) {
+            const int t = (j0 + j) * kFN + tok;
+            kn = kg = vn = 0.f;
+            bad = false;
+            if (t >= kv_len) return;
+            const int blk = a.block_table[(size_t)b * a.max_blocks + t / kPage];
+            bad = blk < 0 || blk >= a.num_blocks;
+            if (bad) return;
+            const uint8_t* kp = a.kc + ((size_t)blk * a.Hkv + hk) * a.lk.bytes;
+            const uint8_t* vp = a.vc + ((size_t)blk * a.Hkv + hk) * a.lv.bytes;
+            kw.load(kp + r16 * a.lk.code_row + half * 8 * WK);
+            if (PROD) sw.load(kp + a.lk.signs_off + r16 * (kDim / 8) + half * 8);
+            vw.load(vp + r16 * a.lv.code_row + half * 8 * WV);
+            kn = reinterpret_cast<const float*>(kp + a.lk.norm_off)[r16] * a.qscale;
+            if (PROD) kg = reinterpret_cast<const float*>(kp + a.lk.gamma_off)[r16] * a.sscale;
+            vn = reinterpret_cast<const float*>(vp + a.lv.norm_off)[r16] * a.vscale;
+        };
+        fetch(0);
+        const uint32_t row = (uint32_t)tok * 128 + half * kFHalf;
+        for (int j = 0; j < n; ++j) {
+            const int s = j & 1;
+            if (j > 1 && !mbar_wait_all(bar(kFBKEmpty + s), (uint32_t)(j / 2 - 1) & 1u, abort, kFWaitNs)) {
+                give_up();
+                break;
+            }
+            uint8_t* kt = smem + kFOffK + s * 2 * kFTile + row;
+#pragma unroll
+            for (int c = 0; c < 8; ++c) {
+                const uint32_t at = (uint32_t)(c ^ (tok & 7)) << 4;
+                uint32_t w[4];
+                levels8<WK, LK>(kw.codes(c), a.tk, w);
+                *reinterpret_cast<uint4*>(kt + at) = make_uint4(w[0], w[1], w[2], w[3]);
+                if (PROD) {
+                    signs8(sw.codes(c), 0x3C003C00u, w);
+                    *reinterpret_cast<uint4*>(kt + kFTile + at) = make_uint4(w[0], w[1], w[2], w[3]);
+                }
+            }
+            if (half == 0) {
+                reinterpret_cast<float2*>(smem + kFOffScal)[s * 128 + tok] = make_float2(kn, kg);
+                if (r16 == 0) {
+                    page_bad[8 * s + tok / kPage] = bad;
+                    if (bad) atomicOr(a.err, TQ_DEVERR_BLOCK);
+                }
+            }
+            fence_proxy_async_shared();
+            mbar_arrive_lead(lead, bar(kFBKFull + s));
+            // the values of a token that is not finite are left out here and make the rows that
+            // attend it NaN at the end: a masked one must not reach any
+            const bool fine = isfinite(vn);
+            if (!fine && half == 0) atomicMin(first_bad, (j0 + j) * kFN + tok);
+            const __half2 v2 = __float2half2_rn(fine ? vn : 0.f);
+            if (j > 0 && !mbar_wait_all(bar(kFBO), (uint32_t)(j - 1) & 1u, abort, kFWaitNs)) {
+                give_up();
+                break;
+            }
+            uint8_t* vt = smem + kFOffV + row;
+#pragma unroll
+            for (int c = 0; c < 8; ++c) {
+                uint32_t w[4];
+                levels8<WV, LV>(vw.codes(c), a.tv, w);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const __half2 x = __hmul2(*reinterpret_cast<const __half2*>(&w[i]), v2);
+                    w[i] = *reinterpret_cast<const uint32_t*>(&x);
+                }
+                *reinterpret_cast<uint4*>(vt + ((uint32_t)(c ^ (tok & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+            fence_proxy_async_shared();
+            mbar_arrive_lead(lead, bar(kFBVFull));
+            if (j + 1 < n) fetch(j + 1);
+        }
+    } else if (warp >= 12) {
+        set_registers_down<kFIssueRegs>();
+        if (warp == 12) {
+        // ------------------------------------------------------------ MMA issuer (converged warp)
+        constexpr uint32_t id_s = idesc_f16(128, kFN), id_o = idesc_f16(128, kDim) | (1u << 16);
+        const uint32_t lead = elect_lane();
+        const uint32_t q_lo = sw128_desc_lo(sbase + kFOffQ), k_lo = sw128_desc_lo(sbase + kFOffK);
+        // the values as they lie, N-major: 64-coordinate blocks kFHalf apart
+        const uint32_t v_lo = (((sbase + kFOffV) >> 4) & 0x3FFFu) | ((kFHalf >> 4) << 16);
+        auto wait = [&](int i, int phase) -> bool {
+            if (mbar_wait_all(bar(i), (uint32_t)phase & 1u, abort, kFWaitNs)) return true;
+            if (lane == 0) give_up();
+            return false;
+        };
+        auto values = [&](int j) {
+#pragma unroll
+            for (int ks = 0; ks < 8; ++ks)
+                umma_ts_warp(lead, kFColO, kFColP + ks * 8, sw128_desc(v_lo + ks * (2048 >> 4)), id_o, (j | ks) > 0);
+            umma_commit_warp(lead, bar(kFBO));
+        };
+        bool ok = tmem == 0;
+        if (!ok && lane == 0) {
+            *abort = 1;
+            atomicOr(a.err, TQ_DEVERR_INTERNAL);
+        }
+        ok = ok && wait(kFBQ, 0);
+        for (int j = 0; ok && j < n; ++j) {
+            ok = wait(kFBKFull + (j & 1), j / 2) && (j == 0 || wait(kFBL, j - 1));
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t kl = k_lo + (j & 1) * (2 * kFTile >> 4);
+#pragma unroll
+            for (int ks = 0; ks < 8; ++ks) {
+                const uint32_t o = (uint32_t)(ks & 3) * 2 + (uint32_t)(ks >> 2) * (kFHalf >> 4);
+                umma_ss_warp(lead, 0, sw128_desc(q_lo + o), sw128_desc(kl + o), id_s, ks > 0);
+                if (PROD)
+                    umma_ss_warp(lead, kFColS2, sw128_desc(q_lo + (kFTile >> 4) + o), sw128_desc(kl + (kFTile >> 4) + o),
+                                 id_s, ks > 0);
+            }
+            umma_commit_warp(lead, bar(kFBS));
+            umma_commit_warp(lead, bar(kFBKEmpty + (j & 1)));
+            if (j > 0) {
+                ok = wait(kFBP, j - 1) && wait(kFBVFull, j - 1);
+                if (!ok) break;
+                tc_fence_after();
+                values(j - 1);
+            }
+        }
+        if (ok) ok = wait(kFBP, n - 1) && wait(kFBVFull, n - 1);
+        if (ok) {
+            tc_fence_after();
+            values(n - 1);
+        }
+        umma_commit_warp(lead, bar(kFBDrain));
+        const volatile int never = 0;
+        mbar_wait(bar(kFBQ), 0, &never, kFWaitNs);
+        mbar_wait(bar(kFBDrain), 0, &never, kFWaitNs);
+        __syncwarp();
+        }
+    } else {
+        set_registers_up<kFSoftmaxRegs>();
+        if (warp < live_warps) {
+        // ------------------------------------------------------------ softmax
+        const int row = threadIdx.x;
+        const uint32_t lanes = (uint32_t)warp << 21, lead = lane == 0;
+        const uint32_t ts = tmem + lanes, tp = tmem + kFColP + lanes, to = tmem + kFColO + lanes;
+        const bool live = row < nrows;
+        const int limit = live ? off + q0 + row / a.G - j0 * kFN : -1;  // its last token, from the split's first
+        const int masked_from = (off + q0 + 1) / kFN - j0;             // first tile with a masked pair
+        float m = -INFINITY;
+        float2 sum[2] = {{0.f, 0.f}, {0.f, 0.f}};
+        bool ok = true;
+        auto wait = [&](int x, int phase) -> bool {
+            if (mbar_wait_all(bar(x), (uint32_t)phase & 1u, abort, kFWaitNs)) return true;
+            give_up();
+            return false;
+        };
+        for (int j = 0; j < n; ++j) {
+            ok = wait(kFBS, j);
+            if (!ok) break;
+            tc_fence_after();
+            uint32_t s[4][32];
+            const float4* sc = reinterpret_cast<const float4*>(smem + kFOffScal) + (j & 1) * 64;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                uint32_t d2[32];
+                tmem_ld32(ts + 32 * q, s[q]);
+                if (PROD) tmem_ld32(ts + kFColS2 + 32 * q, d2);
+                tmem_ld_wait();
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    const float4 f = sc[16 * q + e];  // a, b of two tokens
+                    float x = f.x * __uint_as_float(s[q][2 * e]), y = f.z * __uint_as_float(s[q][2 * e + 1]);
+                    if (PROD) {
+                        x = fmaf(f.y, __uint_as_float(d2[2 * e]), x);
+                        y = fmaf(f.w, __uint_as_float(d2[2 * e + 1]), y);
+                    }
+                    s[q][2 * e] = __float_as_uint(x);
+                    s[q][2 * e + 1] = __float_as_uint(y);
+                }
+            }
+            const uint2 pb = *reinterpret_cast<const uint2*>(page_bad + 8 * (j & 1));
+            tc_fence_before();
+            mbar_arrive_lead(lead, bar(kFBL));
+            mbar_arrive_lead(lead, bar(kFBKEmpty + (j & 1)));
+            if (j >= masked_from) {
+                const int lim = limit - j * kFN;
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+#pragma unroll
+                    for (int e = 0; e < 32; ++e)
+                        if (32 * q + e > lim) s[q][e] = 0xFF800000u;  // -inf
+            }
+            if (pb.x | pb.y) {
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+#pragma unroll
+                    for (int e = 0; e < 32; ++e)
+                        if (((q < 2 ? pb.x : pb.y) >> (8 * (2 * (q & 1) + e / 16))) & 1u) s[q][e] = 0xFF800000u;
+            }
+            float mx[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                mx[q] = few_max3(__uint_as_float(s[q][0]), __uint_as_float(s[q][1]), __uint_as_float(s[q][2]));
+#pragma unroll
+                for (int e = 3; e < 31; e += 2)
+                    mx[q] = few_max3(mx[q], __uint_as_float(s[q][e]), __uint_as_float(s[q][e + 1]));
+                mx[q] = few_max3(mx[q], mx[q], __uint_as_float(s[q][31]));
+            }
+            float top = few_max3(few_max3(mx[0], mx[1], mx[2]), mx[3], mx[3]);
+            // a NaN or infinite score makes the row's sum and outputs NaN; the maximum carries it
+            if (!(top < INFINITY)) top = NAN;
+            const bool grow = top > m + kFRescale || (m == -INFINITY && top > m) || (top != top && m == m);
+            // the tile before is in O, and its P has been read
+            if (j > 0) ok = wait(kFBO, j - 1);
+            if (!ok) break;
+            if (__any_sync(0xffffffffu, grow)) {
+                const float mn = grow ? top : m;
+                if (j > 0) {
+                    const float f = grow ? few_ex2(m - mn) : 1.f;  // (first maximum: ex2(-inf) = 0)
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) sum[q] = __fmul2_rn(sum[q], make_float2(f, f));
+                    tc_fence_after();
+#pragma unroll 1
+                    for (int q = 0; q < 8; ++q) {
+                        uint32_t o[16];
+                        tmem_ld16(to + 16 * q, o);
+                        tmem_ld_wait();
+                        uint32_t lo[8], hi[8];
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            lo[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                            hi[e] = __float_as_uint(__uint_as_float(o[8 + e]) * f);
+                        }
+                        tmem_st8(to + 16 * q, lo);
+                        tmem_st8(to + 16 * q + 8, hi);
+                    }
+                }
+                m = mn;
+            }
+            const float mm = m == -INFINITY ? 0.f : m;
+            const float2 nm = make_float2(-mm, -mm);
+#pragma unroll
+            for (int q = 0; q < 8; ++q) {
+                uint32_t p[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const int i = 16 * q + 2 * e;
+                    float2 x = make_float2(__uint_as_float(s[i / 32][i % 32]), __uint_as_float(s[i / 32][i % 32 + 1]));
+                    x = __fadd2_rn(x, nm);
+                    x.x = few_ex2(x.x);
+                    x.y = few_ex2(x.y);
+                    sum[e & 1] = __fadd2_rn(sum[e & 1], x);
+                    const __half2 hp = __floats2half2_rn(x.x, x.y);
+                    p[e] = *reinterpret_cast<const uint32_t*>(&hp);
+                }
+                tmem_st8(tp + 8 * q, p);
+            }
+            tmem_st_wait();
+            tc_fence_before();
+            mbar_arrive_lead(lead, bar(kFBP));
+        }
+        if (ok) ok = wait(kFBO, n - 1);
+        const float l = (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+        const size_t prow = live ? prow0 + out_row(row) : 0;
+        if (live) {
+            const bool hit = limit + j0 * kFN >= *reinterpret_cast<volatile int*>(first_bad);
+            a.ml[prow] = ok ? make_float2(m, hit ? NAN : l) : make_float2(-INFINITY, 0.f);
+        }
+        if (ok) {
+            tc_fence_after();
+#pragma unroll 1
+            for (int q = 0; q < 4; ++q) {
+                uint32_t o[32];
+                tmem_ld32(to + 32 * q, o);
+                tmem_ld_wait();
+                if (!live) continue;
+                float4* d = reinterpret_cast<float4*>(a.part + prow * kDim + 32 * q);
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    d[i] = make_float4(__uint_as_float(o[4 * i]), __uint_as_float(o[4 * i + 1]),
+                                       __uint_as_float(o[4 * i + 2]), __uint_as_float(o[4 * i + 3]));
+            }
+            tc_fence_before();
+        }
+        }
+    }
+    __syncthreads();
+    if (warp == 12) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+// ---------------------------------------------------------------- rotation of the queries
+// q' = R^T q and s = S q of 64 rows per CTA, 16 per warp, on mma.sync (m16n8k16); R^T as fp16
+// hi + lo, fp32 sums, rounded once.  The matrices' 16-byte pieces lie at k ^ (row % 8).
+constexpr int kRotThreads = 128, kRotRows = 64;
+constexpr uint32_t kRotSmem = 3 * kDim * kDim * 2;
+
+__device__ __forceinline__ uint32_t rot_word(const uint8_t* m, int r, int w) {
+    return *reinterpret_cast<const uint32_t*>(m + r * 256 + ((((w >> 2) ^ (r & 7)) << 4) | ((w & 3) << 2)));
+}
+
+__global__ void __launch_bounds__(kRotThreads) few_rotate_kernel(const uint16_t* q, long long rows, const uint16_t* RTh,
+                                                                 const uint16_t* RTl, const uint16_t* Sh, int prod,
+                                                                 uint16_t* out) {
+    extern __shared__ __align__(16) uint8_t smem[];
+    const uint32_t base = smem_u32(smem);
+    const uint16_t* src[3] = {RTh, RTl, Sh};
+    const int pieces = kDim * kDim * 2 / 16;
+    for (int i = threadIdx.x; i < (prod ? 3 : 2) * pieces; i += kRotThreads) {
+        const int mtx = i / pieces, o = (i - mtx * pieces) * 16, r = o >> 8, k16 = (o >> 4) & 15;
+        cp_async16(base + mtx * (pieces * 16) + r * 256 + ((k16 ^ (r & 7)) << 4),
+                   reinterpret_cast<const uint8_t*>(src[mtx]) + o);
+    }
+    cp_async_commit();
+    const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
+    const long long i0 = (long long)blockIdx.x * kRotRows + 16 * (threadIdx.x >> 5) + g, i1 = i0 + 8;
+    const bool r0 = i0 < rows, r1 = i1 < rows;
+    const uint32_t* q0 = reinterpret_cast<const uint32_t*>(q + (r0 ? i0 : 0) * kDim);
+    const uint32_t* q1 = reinterpret_cast<const uint32_t*>(q + (r1 ? i1 : 0) * kDim);
+    uint32_t qa[8][4];
+#pragma unroll
+    for (int ks = 0; ks < 8; ++ks) {
+        qa[ks][0] = r0 ? q0[8 * ks + c] : 0u;
+        qa[ks][1] = r1 ? q1[8 * ks + c] : 0u;
+        qa[ks][2] = r0 ? q0[8 * ks + c + 4] : 0u;
+        qa[ks][3] = r1 ? q1[8 * ks + c + 4] : 0u;
+    }
+    cp_async_wait<0>();
+    __syncthreads();
+#pragma unroll 1
+    for (int nt = 0; nt < 16; ++nt) {  // output coordinates 8 nt .. 8 nt + 7
+        const int n = 8 * nt + g;
+        float dq[4] = {0.f, 0.f, 0.f, 0.f}, ds[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const uint8_t* lo = smem + kDim * kDim * 2;
+            mma16816(dq, qa[k][0], qa[k][1], qa[k][2], qa[k][3], rot_word(lo, n, 8 * k + c), rot_word(lo, n, 8 * k + c + 4));
+            mma16816(dq, qa[k][0], qa[k][1], qa[k][2], qa[k][3], rot_word(smem, n, 8 * k + c), rot_word(smem, n, 8 * k + c + 4));
+            if (prod) {
+                const uint8_t* sm = smem + 2 * kDim * kDim * 2;
+                mma16816(ds, qa[k][0], qa[k][1], qa[k][2], qa[k][3], rot_word(sm, n, 8 * k + c), rot_word(sm, n, 8 * k + c + 4));
+            }
+        }
+        uint32_t* o0 = reinterpret_cast<uint32_t*>(out + i0 * 2 * kDim) + 4 * nt + c;
+        uint32_t* o1 = reinterpret_cast<uint32_t*>(out + i1 * 2 * kDim) + 4 * nt + c;
+        if (r0) {
+            o0[0] = f2h2(dq[0], dq[1]);
+            if (prod) o0[kDim / 2] = f2h2(ds[0], ds[1]);
+        }
+        if (r1) {
+            o1[0] = f2h2(dq[2], dq[3]);
+            if (prod) o1[kDim / 2] = f2h2(ds[2], ds[3]);
+        }
+    }
+}
+
+// ---------------------------------------------------------------- joining and un-rotation
+// Four rows per warp: o = R (sum_s 2^(m_s - m) acc_s) / l.  R^T (fp32) in shared memory, a lane
+// takes four output coordinates.
+struct JoinArgs {
+    const float* part;
+    const float2* ml;
+    int splits;
+    const int32_t* cu_q;
+    const int32_t* seq_lens;
+    int B, total_q, Hq, max_kv;
+    const float* RT;
+    void* out;
+    int out_fp32;
+};
+constexpr int kJoinThreads = 256, kJoinRows = 32;
+constexpr uint32_t kJoinSmem = kDim * kDim * 4 + kJoinRows * kDim * 4;
+
+__global__ void __launch_bounds__(kJoinThreads) few_join_kernel(const JoinArgs a) {
+    extern __shared__ __align__(16) uint8_t smem[];
+    const uint32_t base = smem_u32(smem);
+    for (int i = threadIdx.x; i < kDim * kDim / 4; i += kJoinThreads) cp_async16(base + 16 * i, a.RT + 4 * i);
+    cp_async_commit();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    float* acc = reinterpret_cast<float*>(smem + kDim * kDim * 4) + warp * 4 * kDim;
+    const size_t rows = (size_t)a.total_q * a.Hq;
+    bool live[4];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+        const size_t row = (size_t)blockIdx.x * kJoinRows + 4 * warp + r;
+        live[r] = false;
+        if (row >= rows) continue;  // (uniform in the warp)
+        const int qi = (int)(row / a.Hq);
+        const int b = find_row_seq(a.cu_q, a.B, qi, lane);
+        const int c0 = a.cu_q[b], c1 = a.cu_q[b + 1], len = a.seq_lens[b];
+        live[r] = qi >= c0 && qi < c1 && c0 >= 0 && c1 <= a.total_q && len >= c1 - c0 && len <= a.max_kv;
+        if (!live[r]) continue;
+        float m = -INFINITY;
+        for (int s = 0; s < a.splits; ++s) {
+            const float2 x = a.ml[s * rows + row];
+            if (x.y != 0.f) m = fmaxf(m, x.x);
+        }
+        float l = 0.f;
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int s = 0; s < a.splits; ++s) {
+            const float2 x = a.ml[s * rows + row];
+            if (x.y == 0.f) continue;  // no token of the row in this split: its sums were not written
+            const float f = exp2f(x.x - (m == -INFINITY ? 0.f : m));
+            const float4 v = reinterpret_cast<const float4*>(a.part + (s * rows + row) * kDim)[lane];
+            l += f * x.y;
+            o.x = fmaf(f, v.x, o.x);
+            o.y = fmaf(f, v.y, o.y);
+            o.z = fmaf(f, v.z, o.z);
+            o.w = fmaf(f, v.w, o.w);
+        }
+        const float inv = l != 0.f ? 1.f / l : 0.f;
+        reinterpret_cast<float4*>(acc + r * kDim)[lane] = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+    }
+    cp_async_wait<0>();
+    __syncthreads();
+    float4 o[4] = {};
+    const float4* RT = reinterpret_cast<const float4*>(smem) + lane;
+#pragma unroll 4
+    for (int j = 0; j < kDim; ++j) {
+        const float4 w = RT[j * (kDim / 4)];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const float x = acc[r * kDim + j];
+            o[r].x = fmaf(w.x, x, o[r].x);
+            o[r].y = fmaf(w.y, x, o[r].y);
+            o[r].z = fmaf(w.z, x, o[r].z);
+            o[r].w = fmaf(w.w, x, o[r].w);
+        }
+    }
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+        if (!live[r]) continue;
+        const size_t row = (size_t)blockIdx.x * kJoinRows + 4 * warp + r;
+        if (a.out_fp32) {
+            reinterpret_cast<float4*>(static_cast<float*>(a.out) + row * kDim)[lane] = o[r];
+        } else {
+            const __half2 p = __floats2half2_rn(o[r].x, o[r].y), q = __floats2half2_rn(o[r].z, o[r].w);
+            reinterpret_cast<uint2*>(static_cast<__half*>(a.out) + row * kDim)[lane] =
+                make_uint2(*reinterpret_cast<const uint32_t*>(&p), *reinterpret_cast<const uint32_t*>(&q));
+        }
+    }
+}
+
+template <int WK, int LK, bool PROD, int WV, int LV>
+cudaError_t launch_few_attend(const CUtensorMap& q, const FewArgs& a, dim3 grid, cudaStream_t stream) {
+    auto k = few_attend_kernel<WK, LK, PROD, WV, LV>;
+    cudaFuncAttributes attr{};
+    cudaError_t e = cudaFuncGetAttributes(&attr, k);
+    if (e != cudaSuccess) return e;
+    if (attr.numRegs != kFRegs) return cudaErrorInvalidConfiguration;  // the register split would not add up
+    e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kFSmem);
+    if (e != cudaSuccess) return e;
+    k<<<grid, kFThreads, kFSmem, stream>>>(q, a);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_chunk_few(const tq_ctx* ctx, const ChunkPlan& plan, const ChunkCall& c, cudaStream_t stream) {
+    uint8_t* ws = c.workspace;
+    const long long most = (long long)c.max_blocks * kPage;
+    const long long rows = (long long)c.total_q * c.Hq;
+    const bool prod = ctx->lay_key.prod;
+    uint16_t* rot = reinterpret_cast<uint16_t*>(ws + plan.k_off);
+    cudaError_t e = cudaFuncSetAttribute(few_rotate_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kRotSmem);
+    if (e != cudaSuccess) return e;
+    const long long rot_blocks = (rows + kRotRows - 1) / kRotRows;
+    if (rot_blocks > 0x7FFFFFFFll) return cudaErrorInvalidValue;
+    few_rotate_kernel<<<(unsigned)rot_blocks, kRotThreads, kRotSmem, stream>>>(c.q, rows, ctx->dev.RTh, ctx->dev.RTl,
+                                                                              ctx->dev.Sh, prod ? 1 : 0, rot);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    count_launches(1);
+
+    FewArgs a{};
+    a.kc = c.kc;
+    a.vc = c.vc;
+    a.num_blocks = c.num_blocks;
+    a.block_table = c.block_table;
+    a.max_blocks = c.max_blocks;
+    a.cu_q = c.cu_q;
+    a.seq_lens = c.seq_lens;
+    a.B = c.B;
+    a.total_q = c.total_q;
+    a.max_kv = (int)(most < c.max_seq_len ? most : c.max_seq_len);
+    a.Hq = c.Hq;
+    a.Hkv = c.Hkv;
+    a.G = c.Hq / c.Hkv;
+    a.QT = 128 / a.G;
+    a.lk = ctx->lay_key;
+    a.lv = ctx->lay_value;
+    a.tk = make_level_table(ctx->cb_key);
+    a.tv = make_level_table(ctx->cb_value);
+    const float scale_log2 = c.scale * 1.4426950408889634f;
+    a.vscale = 1.f / std::sqrt((float)kDim);
+    a.qscale = scale_log2 * a.vscale;
+    a.sscale = scale_log2 * 1.2533141373155003f / (float)kDim;
+    a.part = reinterpret_cast<float*>(ws + plan.part_off);
+    a.ml = reinterpret_cast<float2*>(ws + plan.ml_off);
+    a.out = c.out;
+    a.out_fp32 = c.out_fp32;
+    a.err = ctx->dev_error;
+    CUtensorMap qm;
+    if (!encode_heads_tmap(&qm, rot, c.Hq, c.total_q, (long long)c.Hq * 2 * kDim, a.G, a.QT, 2 * kDim))
+        return cudaErrorInvalidValue;
+    const long long slots = (long long)c.total_q / a.QT + c.B;
+    if (slots * c.Hkv > 0x7FFFFFFFll) return cudaErrorInvalidValue;
+    const dim3 grid((unsigned)(slots * c.Hkv), (unsigned)plan.splits);
+    const int kb = ctx->host.kbits, vb = ctx->host.vbits;
+    if (prod && kb == 3 && vb == 4) e = launch_few_attend<4, 8, true, 4, 16>(qm, a, grid, stream);
+    else if (prod && kb == 2 && vb == 3) e = launch_few_attend<2, 4, true, 4, 8>(qm, a, grid, stream);
+    else if (prod && kb == 1 && vb == 2) e = launch_few_attend<1, 2, true, 2, 4>(qm, a, grid, stream);
+    else if (!prod && kb == 4 && vb == 4) e = launch_few_attend<4, 16, false, 4, 16>(qm, a, grid, stream);
+    else if (!prod && kb == 3 && vb == 3) e = launch_few_attend<4, 8, false, 4, 8>(qm, a, grid, stream);
+    else if (!prod && kb == 2 && vb == 2) e = launch_few_attend<2, 4, false, 2, 4>(qm, a, grid, stream);
+    else return cudaErrorInvalidValue;
+    if (e != cudaSuccess) return e;
+    count_launches(1);
+
+    JoinArgs m{};
+    m.part = a.part;
+    m.ml = a.ml;
+    m.splits = plan.splits;
+    m.cu_q = c.cu_q;
+    m.seq_lens = c.seq_lens;
+    m.B = c.B;
+    m.total_q = c.total_q;
+    m.Hq = c.Hq;
+    m.max_kv = a.max_kv;
+    m.RT = ctx->dev.RT;
+    m.out = c.out;
+    m.out_fp32 = c.out_fp32;
+    e = cudaFuncSetAttribute(few_join_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kJoinSmem);
+    if (e != cudaSuccess) return e;
+    const long long blocks = (rows + kJoinRows - 1) / kJoinRows;
+    few_join_kernel<<<(unsigned)blocks, kJoinThreads, kJoinSmem, stream>>>(m);
+    e = cudaGetLastError();
+    if (e == cudaSuccess) count_launches(1);
+    return e;
+}
+
+}  // namespace tq

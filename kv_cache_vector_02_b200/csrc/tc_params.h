@@ -58,9 +58,9 @@ bool build_tc_blob(const HostParams& H, TcBlob& out);
 // or rejects the arguments.
 bool encode_rows_tmap(CUtensorMap* map, const void* x, int rows);
 
-// TMA descriptor of [rows][heads][128] fp16 vectors, rows `stride` elements apart (a
+// TMA descriptor of [rows][heads][dim] fp16 vectors, rows `stride` elements apart (a
 // multiple of 8), boxes of 64 columns x box_heads x box_rows with the 128-byte swizzle.
 bool encode_heads_tmap(CUtensorMap* map, const void* x, int heads, long long rows, long long stride, int box_heads,
-                       int box_rows);
+                       int box_rows, int dim = 128);
 
 }  // namespace tq

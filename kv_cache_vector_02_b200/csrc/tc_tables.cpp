@@ -199,10 +199,10 @@ bool encode_rows_tmap(CUtensorMap* map, const void* x, int rows) {
 }
 
 bool encode_heads_tmap(CUtensorMap* map, const void* x, int heads, long long rows, long long stride, int box_heads,
-                       int box_rows) {
+                       int box_rows, int dim) {
     if (!find_encode() || rows < 1 || heads < 1) return false;
-    cuuint64_t dims[3] = {cuuint64_t(kD), cuuint64_t(heads), cuuint64_t(rows)};
-    cuuint64_t strides[2] = {cuuint64_t(kD) * 2, cuuint64_t(stride) * 2};
+    cuuint64_t dims[3] = {cuuint64_t(dim), cuuint64_t(heads), cuuint64_t(rows)};
+    cuuint64_t strides[2] = {cuuint64_t(dim) * 2, cuuint64_t(stride) * 2};
     cuuint32_t box[3] = {64, cuuint32_t(box_heads), cuuint32_t(box_rows)};
     cuuint32_t estr[3] = {1, 1, 1};
     const CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<void*>(x), dims, strides, box,

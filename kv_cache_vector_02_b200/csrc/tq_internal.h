@@ -175,10 +175,11 @@ struct AttendCall {
 cudaError_t launch_attend(const tq_ctx* ctx, const AttendCall& c, cudaStream_t stream);
 // A chunk call's way through its workspace (chunk.cu).
 struct ChunkPlan {
+    bool few;            // few rows: straight over the packed pages (chunk_few.cu)
     int kv_pad;          // tokens of a sequence, rounded up to whole tiles of 128
     int heads;           // kv heads decompressed at a time
     int splits;          // of the tokens, in the attention
-    size_t k_off, v_off; // workspace offsets (bytes): fp16 [B * kv_pad][heads][128]
+    size_t k_off, v_off; // workspace offsets (bytes): fp16 [B * kv_pad][heads][128] (few: k_off, rotated queries)
     size_t pages_off;    // u8 [B][kv_pad / 128]
     size_t part_off, ml_off;
     size_t bytes;
@@ -199,6 +200,7 @@ struct ChunkCall {
     int out_fp32;
     uint8_t* workspace;
 };
+cudaError_t launch_chunk_few(const tq_ctx* ctx, const ChunkPlan& plan, const ChunkCall& c, cudaStream_t stream);
 cudaError_t launch_chunk(const tq_ctx* ctx, const ChunkPlan& plan, const ChunkCall& c, cudaStream_t stream);
 cudaError_t launch_decode(const tq_ctx* ctx, const DecodePlan& plan, const uint16_t* q, const uint8_t* kc,
                           const uint8_t* vc, int num_blocks, const int32_t* block_table, int max_blocks,
