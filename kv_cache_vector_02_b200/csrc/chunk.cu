@@ -432,7 +432,10 @@ ChunkPlan plan_chunk(const tq_ctx* ctx, int B, int total_q, int Hq, int Hkv, int
     }
     // Splits of the tokens: as many as make the waves over the SMs shortest, each split
     // costing about three tiles more (its start and end, and its part of the join).
-    const int G = Hq / Hkv, QC = (p.few ? 1 : 2) * (128 / G);
+    const int G = Hq / Hkv;
+    // rows per CTA: 32 where a sequence has no more on average (chunk_few.cu has more buffers then)
+    p.rows = !p.few ? 256 : G <= 32 && (long long)total_q * G <= 32ll * B ? 32 : 128;
+    const int QC = p.few ? p.rows / G : 2 * (128 / G);
     long long ctas = (total_q + QC - 1) / QC;
     if (ctas < B) ctas = B;
     ctas *= p.heads;

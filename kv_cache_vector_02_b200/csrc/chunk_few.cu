@@ -41,13 +41,22 @@ constexpr int kFThreads = 512;
 // Registers: 128 a thread at launch (the launch checks it), moved to the softmax.
 constexpr int kFRegs = 128, kFSoftmaxRegs = 208, kFCodeRegs = 112, kFIssueRegs = 80;
 static_assert(kFSoftmaxRegs + 2 * kFCodeRegs + kFIssueRegs == 4 * kFRegs, "the block's own registers");
-constexpr uint32_t kFOffQ = 0;                      // q' | s, 128 rows each
-constexpr uint32_t kFOffK = 2 * kFTile;             // two buffers of C_k | Sigma
-constexpr uint32_t kFOffV = kFOffK + 4 * kFTile;    // C_v n / sqrt(d)
-constexpr uint32_t kFOffScal = kFOffV + kFTile;     // float2 [2][128]: a_t, b_t
-constexpr uint32_t kFOffBar = kFOffScal + 2 * 128 * 8;
-constexpr uint32_t kFSmem = kFOffBar + 256;
-static_assert(kFSmem <= 232448, "shared memory budget");
+// Shared memory.  At most 32 rows (ROWS = 32): a 64-column block of Q' is 32 rows of 128 bytes,
+// and the MMA's other rows read whatever follows (results that nothing looks at); what that
+// saves holds a second buffer of values.
+template <int ROWS>
+struct FewSmem {
+    static constexpr int kVBufs = ROWS == 32 ? 2 : 1;
+    static constexpr uint32_t kBlock = ROWS * 128;             // 64 columns of Q'
+    static constexpr uint32_t kOffQ = 0;                       // q' | s: two blocks each
+    static constexpr uint32_t kOffK = 4 * kBlock;              // two buffers of C_k | Sigma
+    static constexpr uint32_t kOffV = kOffK + 4 * kFTile;      // C_v n / sqrt(d)
+    static constexpr uint32_t kOffScal = kOffV + kVBufs * kFTile;  // float [2][2][128]: a_t, b_t
+    static constexpr uint32_t kOffBar = kOffScal + 2 * 2 * 128 * 4;
+    static constexpr uint32_t kBytes = kOffBar + 256;
+    static_assert(kBytes <= 232448, "shared memory budget");
+    static_assert(kOffK % 1024 == 0 && kBlock % 1024 == 0, "swizzled tiles");
+};
 constexpr uint64_t kFWaitNs = 2000000000ull;
 constexpr float kFRescale = 8.f;  // log2 of what P may grow to before O is rescaled
 constexpr uint32_t kFColS2 = 128, kFColO = 256, kFColP = 384;
@@ -56,13 +65,14 @@ enum : int {
     kFBQ = 0,
     kFBKFull = 1,   // +buffer
     kFBKEmpty = 3,  // +buffer
-    kFBVFull = 5,
-    kFBO = 6,       // a tile's P V added (and its values read)
-    kFBS = 7,       // scores in tensor memory
-    kFBL = 8,       // scores in registers
-    kFBP = 9,       // P in tensor memory
-    kFBDrain = 10,
-    kFNumBars = 11
+    kFBVFull = 5,   // +buffer
+    kFBVEmpty = 7,  // +buffer
+    kFBO = 9,       // a tile's P V added
+    kFBS = 10,      // scores in tensor memory
+    kFBL = 11,      // scores in registers
+    kFBP = 12,      // P in tensor memory
+    kFBDrain = 13,
+    kFNumBars = 14
 };
 
 struct FewArgs {
@@ -74,7 +84,7 @@ struct FewArgs {
     const int32_t* cu_q;
     const int32_t* seq_lens;
     int B, total_q, max_kv;
-    int Hq, Hkv, G, QT;      // QT = 128 / G queries per CTA
+    int Hq, Hkv, G, QT;      // QT = ROWS / G queries per CTA
     ChunkLayout lk, lv;
     LevelTable tk, tv;
     float qscale, sscale;    // scale log2(e) / sqrt(d), scale log2(e) sqrt(pi/2) / d
@@ -125,9 +135,10 @@ struct HalfRow {
     __device__ __forceinline__ uint32_t codes(int c) const { return w[8 * W * c / 32] >> (8 * W * c % 32); }
 };
 
-template <int WK, int LK, bool PROD, int WV, int LV>
+template <int ROWS, int WK, int LK, bool PROD, int WV, int LV>
 __global__ void __launch_bounds__(kFThreads, 1)
     few_attend_kernel(const __grid_constant__ CUtensorMap q_map, const FewArgs a) {
+    using M = FewSmem<ROWS>;
     extern __shared__ __align__(1024) uint8_t smem[];
     const uint32_t sbase = smem_u32(smem);
     const int warp = __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
@@ -135,6 +146,8 @@ __global__ void __launch_bounds__(kFThreads, 1)
         if (threadIdx.x == 0) atomicOr(a.err, TQ_DEVERR_INTERNAL);
         return;
     }
+    griddep_wait();  // (nothing above depends on an earlier kernel)
+    griddep_launch_dependents();
     const int slot = (int)(blockIdx.x / (unsigned)a.Hkv), hk = (int)(blockIdx.x % (unsigned)a.Hkv);
     if (blockIdx.x == 0 && blockIdx.y == 0) {
         for (int b = threadIdx.x; b < a.B; b += kFThreads)
@@ -171,12 +184,12 @@ __global__ void __launch_bounds__(kFThreads, 1)
     }
     const int live_warps = (nrows + 31) / 32;
 
-    const uint32_t bars = sbase + kFOffBar;
+    const uint32_t bars = sbase + M::kOffBar;
     auto bar = [&](int i) -> uint32_t { return bars + 8u * (uint32_t)i; };
-    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + kFOffBar + 8 * kFNumBars);
-    volatile int* abort = reinterpret_cast<volatile int*>(smem + kFOffBar + 8 * kFNumBars + 4);
-    int* first_bad = reinterpret_cast<int*>(smem + kFOffBar + 8 * kFNumBars + 8);
-    uint8_t* page_bad = smem + kFOffBar + 8 * kFNumBars + 16;  // [2][8]
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + M::kOffBar + 8 * kFNumBars);
+    volatile int* abort = reinterpret_cast<volatile int*>(smem + M::kOffBar + 8 * kFNumBars + 4);
+    int* first_bad = reinterpret_cast<int*>(smem + M::kOffBar + 8 * kFNumBars + 8);
+    uint8_t* page_bad = smem + M::kOffBar + 8 * kFNumBars + 16;  // [2][8]
     auto give_up = [&] {
         *abort = 1;
         atomicOr(a.err, TQ_DEVERR_TIMEOUT);
@@ -187,7 +200,10 @@ __global__ void __launch_bounds__(kFThreads, 1)
             mbar_init(bar(kFBKFull + s), 8);
             mbar_init(bar(kFBKEmpty + s), (uint32_t)live_warps + 1);  // MMAs done, scalars read
         }
-        mbar_init(bar(kFBVFull), 8);
+        for (int s = 0; s < M::kVBufs; ++s) {
+            mbar_init(bar(kFBVFull + s), 8);
+            mbar_init(bar(kFBVEmpty + s), 1);
+        }
         mbar_init(bar(kFBO), 1);
         mbar_init(bar(kFBS), 1);
         mbar_init(bar(kFBL), (uint32_t)live_warps);
@@ -199,7 +215,7 @@ __global__ void __launch_bounds__(kFThreads, 1)
         const int box = a.G * a.QT * 128;
         mbar_arrive_expect_tx(bar(kFBQ), (uint32_t)(box * (PROD ? 4 : 2)));
         for (int x = 0; x < (PROD ? 4 : 2); ++x)
-            tma_load_3d(sbase + kFOffQ + x * kFHalf, &q_map, 64 * x, hk * a.G, c0 + q0, bar(kFBQ));
+            tma_load_3d(sbase + M::kOffQ + x * M::kBlock, &q_map, 64 * x, hk * a.G, c0 + q0, bar(kFBQ));
     }
     if (warp == 12) {
         tmem_alloc(smem_u32(tmem_slot), 512);
@@ -215,71 +231,81 @@ __global__ void __launch_bounds__(kFThreads, 1)
         // ------------------------------------------------------------ codes to operands
         const int tok = threadIdx.x & 127, half = warp >= 8 ? 1 : 0, r16 = tok % kPage;
         const uint32_t lead = lane == 0;
-        HalfRow<WK> kw{};
-        HalfRow<WV> vw{};
-        HalfRow<1> sw{};
-        float kn = 0.f, kg = 0.f, vn = 0.f;
-        bool bad = false;
-        auto fetch = [&](int j) {
+        struct Raw {  // a tile's packed bytes of this thread's half token
+            HalfRow<WK> kw;
+            HalfRow<WV> vw;
+            HalfRow<1> sw;
+            float kn, kg, vn;
+            bool bad;
+        };
+        // block of the thread's token in tile j: -1 behind the last token, -2 out of range
+        auto block_of = [&](int j) -> int {
             const int t = (j0 + j) * kFN + tok;
-            kn = kg = vn = 0.f;
-            bad = false;
-            if (t >= kv_len) return;
+            if (j >= n || t >= kv_len) return -1;
             const int blk = a.block_table[(size_t)b * a.max_blocks + t / kPage];
-            bad = blk < 0 || blk >= a.num_blocks;
-            if (bad) return;
+            return blk >= 0 && blk < a.num_blocks ? blk : -2;
+        };
+        auto fetch = [&](Raw& r, int blk) {
+            r.kn = r.kg = r.vn = 0.f;
+            r.bad = blk == -2;
+            if (blk < 0) return;
             const uint8_t* kp = a.kc + ((size_t)blk * a.Hkv + hk) * a.lk.bytes;
             const uint8_t* vp = a.vc + ((size_t)blk * a.Hkv + hk) * a.lv.bytes;
-            kw.load(kp + r16 * a.lk.code_row + half * 8 * WK);
-            if (PROD) sw.load(kp + a.lk.signs_off + r16 * (kDim / 8) + half * 8);
-            vw.load(vp + r16 * a.lv.code_row + half * 8 * WV);
-            kn = reinterpret_cast<const float*>(kp + a.lk.norm_off)[r16] * a.qscale;
-            if (PROD) kg = reinterpret_cast<const float*>(kp + a.lk.gamma_off)[r16] * a.sscale;
-            vn = reinterpret_cast<const float*>(vp + a.lv.norm_off)[r16] * a.vscale;
+            r.kw.load(kp + r16 * a.lk.code_row + half * 8 * WK);
+            if (PROD) r.sw.load(kp + a.lk.signs_off + r16 * (kDim / 8) + half * 8);
+            r.vw.load(vp + r16 * a.lv.code_row + half * 8 * WV);
+            r.kn = reinterpret_cast<const float*>(kp + a.lk.norm_off)[r16];
+            if (PROD) r.kg = reinterpret_cast<const float*>(kp + a.lk.gamma_off)[r16];
+            r.vn = reinterpret_cast<const float*>(vp + a.lv.norm_off)[r16];
         };
-        fetch(0);
         const uint32_t row = (uint32_t)tok * 128 + half * kFHalf;
-        for (int j = 0; j < n; ++j) {
-            const int s = j & 1;
+        bool ok = true;
+        auto tile = [&](const Raw& r, int j, int s) {
             if (j > 1 && !mbar_wait_all(bar(kFBKEmpty + s), (uint32_t)(j / 2 - 1) & 1u, abort, kFWaitNs)) {
                 give_up();
-                break;
+                ok = false;
+                return;
             }
-            uint8_t* kt = smem + kFOffK + s * 2 * kFTile + row;
+            uint8_t* kt = smem + M::kOffK + s * 2 * kFTile + row;
 #pragma unroll
             for (int c = 0; c < 8; ++c) {
                 const uint32_t at = (uint32_t)(c ^ (tok & 7)) << 4;
                 uint32_t w[4];
-                levels8<WK, LK>(kw.codes(c), a.tk, w);
+                levels8<WK, LK>(r.kw.codes(c), a.tk, w);
                 *reinterpret_cast<uint4*>(kt + at) = make_uint4(w[0], w[1], w[2], w[3]);
                 if (PROD) {
-                    signs8(sw.codes(c), 0x3C003C00u, w);
+                    signs8(r.sw.codes(c), 0x3C003C00u, w);
                     *reinterpret_cast<uint4*>(kt + kFTile + at) = make_uint4(w[0], w[1], w[2], w[3]);
                 }
             }
             if (half == 0) {
-                reinterpret_cast<float2*>(smem + kFOffScal)[s * 128 + tok] = make_float2(kn, kg);
+                float* scal = reinterpret_cast<float*>(smem + M::kOffScal) + s * 256 + tok;
+                scal[0] = r.kn * a.qscale;
+                if (PROD) scal[128] = r.kg * a.sscale;
                 if (r16 == 0) {
-                    page_bad[8 * s + tok / kPage] = bad;
-                    if (bad) atomicOr(a.err, TQ_DEVERR_BLOCK);
+                    page_bad[8 * s + tok / kPage] = r.bad;
+                    if (r.bad) atomicOr(a.err, TQ_DEVERR_BLOCK);
                 }
             }
             fence_proxy_async_shared();
             mbar_arrive_lead(lead, bar(kFBKFull + s));
             // the values of a token that is not finite are left out here and make the rows that
             // attend it NaN at the end: a masked one must not reach any
+            const float vn = r.vn * a.vscale;
             const bool fine = isfinite(vn);
             if (!fine && half == 0) atomicMin(first_bad, (j0 + j) * kFN + tok);
             const __half2 v2 = __float2half2_rn(fine ? vn : 0.f);
-            if (j > 0 && !mbar_wait_all(bar(kFBO), (uint32_t)(j - 1) & 1u, abort, kFWaitNs)) {
+            const int vb = j % M::kVBufs, use = j / M::kVBufs;
+            if (use > 0 && !mbar_wait_all(bar(kFBVEmpty + vb), (uint32_t)(use - 1) & 1u, abort, kFWaitNs)) {
                 give_up();
-                break;
+                ok = false;
+                return;
             }
-            uint8_t* vt = smem + kFOffV + row;
+            uint8_t* vt = smem + M::kOffV + vb * kFTile + row;
 #pragma unroll
             for (int c = 0; c < 8; ++c) {
                 uint32_t w[4];
-                levels8<WV, LV>(vw.codes(c), a.tv, w);
+                levels8<WV, LV>(r.vw.codes(c), a.tv, w);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const __half2 x = __hmul2(*reinterpret_cast<const __half2*>(&w[i]), v2);
@@ -288,8 +314,24 @@ __global__ void __launch_bounds__(kFThreads, 1)
                 *reinterpret_cast<uint4*>(vt + ((uint32_t)(c ^ (tok & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
             }
             fence_proxy_async_shared();
-            mbar_arrive_lead(lead, bar(kFBVFull));
-            if (j + 1 < n) fetch(j + 1);
+            mbar_arrive_lead(lead, bar(kFBVFull + vb));
+        };
+        // a tile's bytes are asked for two tiles ahead, its block id three
+        Raw r0{}, r1{};
+        int blk = block_of(0);
+        int next = block_of(1);
+        fetch(r0, blk);
+        blk = block_of(2);
+        fetch(r1, next);
+#pragma unroll 1
+        for (int j = 0; j < n && ok; j += 2) {
+            next = block_of(j + 3);
+            tile(r0, j, 0);
+            fetch(r0, blk);
+            if (j + 1 >= n || !ok) break;
+            blk = block_of(j + 4);
+            tile(r1, j + 1, 1);
+            fetch(r1, next);
         }
     } else if (warp >= 12) {
         set_registers_down<kFIssueRegs>();
@@ -297,9 +339,9 @@ __global__ void __launch_bounds__(kFThreads, 1)
         // ------------------------------------------------------------ MMA issuer (converged warp)
         constexpr uint32_t id_s = idesc_f16(128, kFN), id_o = idesc_f16(128, kDim) | (1u << 16);
         const uint32_t lead = elect_lane();
-        const uint32_t q_lo = sw128_desc_lo(sbase + kFOffQ), k_lo = sw128_desc_lo(sbase + kFOffK);
+        const uint32_t q_lo = sw128_desc_lo(sbase + M::kOffQ), k_lo = sw128_desc_lo(sbase + M::kOffK);
         // the values as they lie, N-major: 64-coordinate blocks kFHalf apart
-        const uint32_t v_lo = (((sbase + kFOffV) >> 4) & 0x3FFFu) | ((kFHalf >> 4) << 16);
+        const uint32_t v_lo = (((sbase + M::kOffV) >> 4) & 0x3FFFu) | ((kFHalf >> 4) << 16);
         auto wait = [&](int i, int phase) -> bool {
             if (mbar_wait_all(bar(i), (uint32_t)phase & 1u, abort, kFWaitNs)) return true;
             if (lane == 0) give_up();
@@ -308,8 +350,10 @@ __global__ void __launch_bounds__(kFThreads, 1)
         auto values = [&](int j) {
 #pragma unroll
             for (int ks = 0; ks < 8; ++ks)
-                umma_ts_warp(lead, kFColO, kFColP + ks * 8, sw128_desc(v_lo + ks * (2048 >> 4)), id_o, (j | ks) > 0);
+                umma_ts_warp(lead, kFColO, kFColP + ks * 8, sw128_desc(v_lo + (j % M::kVBufs) * (kFTile >> 4) + ks * (2048 >> 4)),
+                             id_o, (j | ks) > 0);
             umma_commit_warp(lead, bar(kFBO));
+            umma_commit_warp(lead, bar(kFBVEmpty + j % M::kVBufs));
         };
         bool ok = tmem == 0;
         if (!ok && lane == 0) {
@@ -325,21 +369,22 @@ __global__ void __launch_bounds__(kFThreads, 1)
 #pragma unroll
             for (int ks = 0; ks < 8; ++ks) {
                 const uint32_t o = (uint32_t)(ks & 3) * 2 + (uint32_t)(ks >> 2) * (kFHalf >> 4);
-                umma_ss_warp(lead, 0, sw128_desc(q_lo + o), sw128_desc(kl + o), id_s, ks > 0);
+                const uint32_t qo = (uint32_t)(ks & 3) * 2 + (uint32_t)(ks >> 2) * (M::kBlock >> 4);
+                umma_ss_warp(lead, 0, sw128_desc(q_lo + qo), sw128_desc(kl + o), id_s, ks > 0);
                 if (PROD)
-                    umma_ss_warp(lead, kFColS2, sw128_desc(q_lo + (kFTile >> 4) + o), sw128_desc(kl + (kFTile >> 4) + o),
-                                 id_s, ks > 0);
+                    umma_ss_warp(lead, kFColS2, sw128_desc(q_lo + (2 * M::kBlock >> 4) + qo),
+                                 sw128_desc(kl + (kFTile >> 4) + o), id_s, ks > 0);
             }
             umma_commit_warp(lead, bar(kFBS));
             umma_commit_warp(lead, bar(kFBKEmpty + (j & 1)));
             if (j > 0) {
-                ok = wait(kFBP, j - 1) && wait(kFBVFull, j - 1);
+                ok = wait(kFBP, j - 1) && wait(kFBVFull + (j - 1) % M::kVBufs, (j - 1) / M::kVBufs);
                 if (!ok) break;
                 tc_fence_after();
                 values(j - 1);
             }
         }
-        if (ok) ok = wait(kFBP, n - 1) && wait(kFBVFull, n - 1);
+        if (ok) ok = wait(kFBP, n - 1) && wait(kFBVFull + (n - 1) % M::kVBufs, (n - 1) / M::kVBufs);
         if (ok) {
             tc_fence_after();
             values(n - 1);
@@ -373,7 +418,7 @@ __global__ void __launch_bounds__(kFThreads, 1)
             if (!ok) break;
             tc_fence_after();
             uint32_t s[4][32];
-            const float4* sc = reinterpret_cast<const float4*>(smem + kFOffScal) + (j & 1) * 64;
+            const float4* sc = reinterpret_cast<const float4*>(smem + M::kOffScal + (j & 1) * 1024);
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
                 uint32_t d2[32];
@@ -381,15 +426,21 @@ __global__ void __launch_bounds__(kFThreads, 1)
                 if (PROD) tmem_ld32(ts + kFColS2 + 32 * q, d2);
                 tmem_ld_wait();
 #pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                    const float4 f = sc[16 * q + e];  // a, b of two tokens
-                    float x = f.x * __uint_as_float(s[q][2 * e]), y = f.z * __uint_as_float(s[q][2 * e + 1]);
+                for (int e = 0; e < 8; ++e) {  // four tokens
+                    const float4 fa = sc[8 * q + e];
+                    uint32_t* x = &s[q][4 * e];
+                    float2 u = __fmul2_rn(make_float2(fa.x, fa.y), make_float2(__uint_as_float(x[0]), __uint_as_float(x[1])));
+                    float2 v = __fmul2_rn(make_float2(fa.z, fa.w), make_float2(__uint_as_float(x[2]), __uint_as_float(x[3])));
                     if (PROD) {
-                        x = fmaf(f.y, __uint_as_float(d2[2 * e]), x);
-                        y = fmaf(f.w, __uint_as_float(d2[2 * e + 1]), y);
+                        const float4 fb = sc[32 + 8 * q + e];
+                        const uint32_t* y = &d2[4 * e];
+                        u = __ffma2_rn(make_float2(fb.x, fb.y), make_float2(__uint_as_float(y[0]), __uint_as_float(y[1])), u);
+                        v = __ffma2_rn(make_float2(fb.z, fb.w), make_float2(__uint_as_float(y[2]), __uint_as_float(y[3])), v);
                     }
-                    s[q][2 * e] = __float_as_uint(x);
-                    s[q][2 * e + 1] = __float_as_uint(y);
+                    x[0] = __float_as_uint(u.x);
+                    x[1] = __float_as_uint(u.y);
+                    x[2] = __float_as_uint(v.x);
+                    x[3] = __float_as_uint(v.y);
                 }
             }
             const uint2 pb = *reinterpret_cast<const uint2*>(page_bad + 8 * (j & 1));
@@ -506,10 +557,11 @@ __global__ void __launch_bounds__(kFThreads, 1)
 }
 
 // ---------------------------------------------------------------- rotation of the queries
-// q' = R^T q and s = S q of 64 rows per CTA, 16 per warp, on mma.sync (m16n8k16); R^T as fp16
-// hi + lo, fp32 sums, rounded once.  The matrices' 16-byte pieces lie at k ^ (row % 8).
-constexpr int kRotThreads = 128, kRotRows = 64;
-constexpr uint32_t kRotSmem = 3 * kDim * kDim * 2;
+// q' = R^T q and s = S q of 64 rows and 32 output coordinates per CTA, 16 rows per warp, on
+// mma.sync (m16n8k16); R^T as fp16 hi + lo, fp32 sums, rounded once.  The matrices' 16-byte
+// pieces lie at k ^ (row % 8).
+constexpr int kRotThreads = 128, kRotRows = 64, kRotCols = 32;
+constexpr uint32_t kRotMat = kRotCols * kDim * 2;
 
 __device__ __forceinline__ uint32_t rot_word(const uint8_t* m, int r, int w) {
     return *reinterpret_cast<const uint32_t*>(m + r * 256 + ((((w >> 2) ^ (r & 7)) << 4) | ((w & 3) << 2)));
@@ -518,16 +570,18 @@ __device__ __forceinline__ uint32_t rot_word(const uint8_t* m, int r, int w) {
 __global__ void __launch_bounds__(kRotThreads) few_rotate_kernel(const uint16_t* q, long long rows, const uint16_t* RTh,
                                                                  const uint16_t* RTl, const uint16_t* Sh, int prod,
                                                                  uint16_t* out) {
-    extern __shared__ __align__(16) uint8_t smem[];
+    __shared__ __align__(16) uint8_t smem[3 * kRotMat];
     const uint32_t base = smem_u32(smem);
     const uint16_t* src[3] = {RTh, RTl, Sh};
-    const int pieces = kDim * kDim * 2 / 16;
+    const int pieces = kRotMat / 16, n0 = blockIdx.y * kRotCols;
     for (int i = threadIdx.x; i < (prod ? 3 : 2) * pieces; i += kRotThreads) {
         const int mtx = i / pieces, o = (i - mtx * pieces) * 16, r = o >> 8, k16 = (o >> 4) & 15;
         cp_async16(base + mtx * (pieces * 16) + r * 256 + ((k16 ^ (r & 7)) << 4),
-                   reinterpret_cast<const uint8_t*>(src[mtx]) + o);
+                   reinterpret_cast<const uint8_t*>(src[mtx]) + n0 * 256 + o);
     }
     cp_async_commit();
+    griddep_wait();  // the queries may come from the kernel before
+    griddep_launch_dependents();
     const int lane = threadIdx.x & 31, g = lane >> 2, c = lane & 3;
     const long long i0 = (long long)blockIdx.x * kRotRows + 16 * (threadIdx.x >> 5) + g, i1 = i0 + 8;
     const bool r0 = i0 < rows, r1 = i1 < rows;
@@ -544,21 +598,21 @@ __global__ void __launch_bounds__(kRotThreads) few_rotate_kernel(const uint16_t*
     cp_async_wait<0>();
     __syncthreads();
 #pragma unroll 1
-    for (int nt = 0; nt < 16; ++nt) {  // output coordinates 8 nt .. 8 nt + 7
+    for (int nt = 0; nt < kRotCols / 8; ++nt) {  // output coordinates n0 + 8 nt .. + 7
         const int n = 8 * nt + g;
         float dq[4] = {0.f, 0.f, 0.f, 0.f}, ds[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
-            const uint8_t* lo = smem + kDim * kDim * 2;
+            const uint8_t* lo = smem + kRotMat;
             mma16816(dq, qa[k][0], qa[k][1], qa[k][2], qa[k][3], rot_word(lo, n, 8 * k + c), rot_word(lo, n, 8 * k + c + 4));
             mma16816(dq, qa[k][0], qa[k][1], qa[k][2], qa[k][3], rot_word(smem, n, 8 * k + c), rot_word(smem, n, 8 * k + c + 4));
             if (prod) {
-                const uint8_t* sm = smem + 2 * kDim * kDim * 2;
+                const uint8_t* sm = smem + 2 * kRotMat;
                 mma16816(ds, qa[k][0], qa[k][1], qa[k][2], qa[k][3], rot_word(sm, n, 8 * k + c), rot_word(sm, n, 8 * k + c + 4));
             }
         }
-        uint32_t* o0 = reinterpret_cast<uint32_t*>(out + i0 * 2 * kDim) + 4 * nt + c;
-        uint32_t* o1 = reinterpret_cast<uint32_t*>(out + i1 * 2 * kDim) + 4 * nt + c;
+        uint32_t* o0 = reinterpret_cast<uint32_t*>(out + i0 * 2 * kDim + n0) + 4 * nt + c;
+        uint32_t* o1 = reinterpret_cast<uint32_t*>(out + i1 * 2 * kDim + n0) + 4 * nt + c;
         if (r0) {
             o0[0] = f2h2(dq[0], dq[1]);
             if (prod) o0[kDim / 2] = f2h2(ds[0], ds[1]);
@@ -571,7 +625,7 @@ __global__ void __launch_bounds__(kRotThreads) few_rotate_kernel(const uint16_t*
 }
 
 // ---------------------------------------------------------------- joining and un-rotation
-// Four rows per warp: o = R (sum_s 2^(m_s - m) acc_s) / l.  R^T (fp32) in shared memory, a lane
+// Two rows per warp: o = R (sum_s 2^(m_s - m) acc_s) / l.  R^T (fp32) in shared memory, a lane
 // takes four output coordinates.
 struct JoinArgs {
     const float* part;
@@ -584,7 +638,7 @@ struct JoinArgs {
     void* out;
     int out_fp32;
 };
-constexpr int kJoinThreads = 256, kJoinRows = 32;
+constexpr int kJoinThreads = 256, kJoinPer = 2, kJoinRows = 8 * kJoinPer;
 constexpr uint32_t kJoinSmem = kDim * kDim * 4 + kJoinRows * kDim * 4;
 
 __global__ void __launch_bounds__(kJoinThreads) few_join_kernel(const JoinArgs a) {
@@ -592,13 +646,14 @@ __global__ void __launch_bounds__(kJoinThreads) few_join_kernel(const JoinArgs a
     const uint32_t base = smem_u32(smem);
     for (int i = threadIdx.x; i < kDim * kDim / 4; i += kJoinThreads) cp_async16(base + 16 * i, a.RT + 4 * i);
     cp_async_commit();
+    griddep_wait();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    float* acc = reinterpret_cast<float*>(smem + kDim * kDim * 4) + warp * 4 * kDim;
+    float* acc = reinterpret_cast<float*>(smem + kDim * kDim * 4) + warp * kJoinPer * kDim;
     const size_t rows = (size_t)a.total_q * a.Hq;
-    bool live[4];
+    bool live[kJoinPer];
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-        const size_t row = (size_t)blockIdx.x * kJoinRows + 4 * warp + r;
+    for (int r = 0; r < kJoinPer; ++r) {
+        const size_t row = (size_t)blockIdx.x * kJoinRows + kJoinPer * warp + r;
         live[r] = false;
         if (row >= rows) continue;  // (uniform in the warp)
         const int qi = (int)(row / a.Hq);
@@ -606,47 +661,57 @@ __global__ void __launch_bounds__(kJoinThreads) few_join_kernel(const JoinArgs a
         const int c0 = a.cu_q[b], c1 = a.cu_q[b + 1], len = a.seq_lens[b];
         live[r] = qi >= c0 && qi < c1 && c0 >= 0 && c1 <= a.total_q && len >= c1 - c0 && len <= a.max_kv;
         if (!live[r]) continue;
-        float m = -INFINITY;
-        for (int s = 0; s < a.splits; ++s) {
-            const float2 x = a.ml[s * rows + row];
-            if (x.y != 0.f) m = fmaxf(m, x.x);
-        }
-        float l = 0.f;
-        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int s = 0; s < a.splits; ++s) {
-            const float2 x = a.ml[s * rows + row];
-            if (x.y == 0.f) continue;  // no token of the row in this split: its sums were not written
-            const float f = exp2f(x.x - (m == -INFINITY ? 0.f : m));
-            const float4 v = reinterpret_cast<const float4*>(a.part + (s * rows + row) * kDim)[lane];
-            l += f * x.y;
-            o.x = fmaf(f, v.x, o.x);
-            o.y = fmaf(f, v.y, o.y);
-            o.z = fmaf(f, v.z, o.z);
-            o.w = fmaf(f, v.w, o.w);
-        }
+        // lane s has split s (32 at most); no token of the row in a split: its sums were not written
+        const float2 x = lane < a.splits ? a.ml[lane * rows + row] : make_float2(-INFINITY, 0.f);
+        float m = x.y != 0.f ? x.x : -INFINITY;
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+        const float f = x.y != 0.f ? exp2f(x.x - (m == -INFINITY ? 0.f : m)) : 0.f;
+        float l = x.y != 0.f ? f * x.y : 0.f;
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
         const float inv = l != 0.f ? 1.f / l : 0.f;
+        uint32_t some = __ballot_sync(0xffffffffu, x.y != 0.f);
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+        const float4* part = reinterpret_cast<const float4*>(a.part + row * kDim) + lane;
+#pragma unroll 4
+        for (int s = 0; s < a.splits; ++s) {
+            const float fs = __shfl_sync(0xffffffffu, f, s);
+            if (!((some >> s) & 1u)) continue;
+            const float4 v = part[s * rows * (kDim / 4)];
+            o.x = fmaf(fs, v.x, o.x);
+            o.y = fmaf(fs, v.y, o.y);
+            o.z = fmaf(fs, v.z, o.z);
+            o.w = fmaf(fs, v.w, o.w);
+        }
         reinterpret_cast<float4*>(acc + r * kDim)[lane] = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
     }
     cp_async_wait<0>();
     __syncthreads();
-    float4 o[4] = {};
+    float4 o[kJoinPer] = {};
     const float4* RT = reinterpret_cast<const float4*>(smem) + lane;
 #pragma unroll 4
-    for (int j = 0; j < kDim; ++j) {
-        const float4 w = RT[j * (kDim / 4)];
+    for (int j = 0; j < kDim; j += 4) {
+        float4 x[kJoinPer];
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            const float x = acc[r * kDim + j];
-            o[r].x = fmaf(w.x, x, o[r].x);
-            o[r].y = fmaf(w.y, x, o[r].y);
-            o[r].z = fmaf(w.z, x, o[r].z);
-            o[r].w = fmaf(w.w, x, o[r].w);
+        for (int r = 0; r < kJoinPer; ++r) x[r] = *reinterpret_cast<const float4*>(acc + r * kDim + j);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float4 w = RT[(j + i) * (kDim / 4)];
+#pragma unroll
+            for (int r = 0; r < kJoinPer; ++r) {
+                const float xi = i == 0 ? x[r].x : i == 1 ? x[r].y : i == 2 ? x[r].z : x[r].w;
+                o[r].x = fmaf(w.x, xi, o[r].x);
+                o[r].y = fmaf(w.y, xi, o[r].y);
+                o[r].z = fmaf(w.z, xi, o[r].z);
+                o[r].w = fmaf(w.w, xi, o[r].w);
+            }
         }
     }
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
+    for (int r = 0; r < kJoinPer; ++r) {
         if (!live[r]) continue;
-        const size_t row = (size_t)blockIdx.x * kJoinRows + 4 * warp + r;
+        const size_t row = (size_t)blockIdx.x * kJoinRows + kJoinPer * warp + r;
         if (a.out_fp32) {
             reinterpret_cast<float4*>(static_cast<float*>(a.out) + row * kDim)[lane] = o[r];
         } else {
@@ -657,17 +722,34 @@ __global__ void __launch_bounds__(kJoinThreads) few_join_kernel(const JoinArgs a
     }
 }
 
-template <int WK, int LK, bool PROD, int WV, int LV>
+// A launch whose setup (what comes before its griddep_wait) may overlap the kernel before.
+template <typename... P, typename... A>
+cudaError_t launch_after(void (*k)(P...), dim3 grid, int threads, uint32_t smem, cudaStream_t stream, const A&... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, k, args...);
+    if (e == cudaSuccess) count_launches(1);
+    return e;
+}
+
+template <int ROWS, int WK, int LK, bool PROD, int WV, int LV>
 cudaError_t launch_few_attend(const CUtensorMap& q, const FewArgs& a, dim3 grid, cudaStream_t stream) {
-    auto k = few_attend_kernel<WK, LK, PROD, WV, LV>;
+    auto k = few_attend_kernel<ROWS, WK, LK, PROD, WV, LV>;
     cudaFuncAttributes attr{};
     cudaError_t e = cudaFuncGetAttributes(&attr, k);
     if (e != cudaSuccess) return e;
     if (attr.numRegs != kFRegs) return cudaErrorInvalidConfiguration;  // the register split would not add up
-    e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kFSmem);
+    e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)FewSmem<ROWS>::kBytes);
     if (e != cudaSuccess) return e;
-    k<<<grid, kFThreads, kFSmem, stream>>>(q, a);
-    return cudaGetLastError();
+    return launch_after(k, grid, kFThreads, FewSmem<ROWS>::kBytes, stream, q, a);
 }
 
 }  // namespace
@@ -678,15 +760,11 @@ cudaError_t launch_chunk_few(const tq_ctx* ctx, const ChunkPlan& plan, const Chu
     const long long rows = (long long)c.total_q * c.Hq;
     const bool prod = ctx->lay_key.prod;
     uint16_t* rot = reinterpret_cast<uint16_t*>(ws + plan.k_off);
-    cudaError_t e = cudaFuncSetAttribute(few_rotate_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kRotSmem);
-    if (e != cudaSuccess) return e;
     const long long rot_blocks = (rows + kRotRows - 1) / kRotRows;
     if (rot_blocks > 0x7FFFFFFFll) return cudaErrorInvalidValue;
-    few_rotate_kernel<<<(unsigned)rot_blocks, kRotThreads, kRotSmem, stream>>>(c.q, rows, ctx->dev.RTh, ctx->dev.RTl,
-                                                                              ctx->dev.Sh, prod ? 1 : 0, rot);
-    e = cudaGetLastError();
+    cudaError_t e = launch_after(few_rotate_kernel, dim3((unsigned)rot_blocks, kDim / kRotCols), kRotThreads, 0, stream, c.q,
+                                 rows, ctx->dev.RTh, ctx->dev.RTl, ctx->dev.Sh, prod ? 1 : 0, rot);
     if (e != cudaSuccess) return e;
-    count_launches(1);
 
     FewArgs a{};
     a.kc = c.kc;
@@ -702,7 +780,7 @@ cudaError_t launch_chunk_few(const tq_ctx* ctx, const ChunkPlan& plan, const Chu
     a.Hq = c.Hq;
     a.Hkv = c.Hkv;
     a.G = c.Hq / c.Hkv;
-    a.QT = 128 / a.G;
+    a.QT = plan.rows / a.G;
     a.lk = ctx->lay_key;
     a.lv = ctx->lay_value;
     a.tk = make_level_table(ctx->cb_key);
@@ -723,15 +801,19 @@ cudaError_t launch_chunk_few(const tq_ctx* ctx, const ChunkPlan& plan, const Chu
     if (slots * c.Hkv > 0x7FFFFFFFll) return cudaErrorInvalidValue;
     const dim3 grid((unsigned)(slots * c.Hkv), (unsigned)plan.splits);
     const int kb = ctx->host.kbits, vb = ctx->host.vbits;
-    if (prod && kb == 3 && vb == 4) e = launch_few_attend<4, 8, true, 4, 16>(qm, a, grid, stream);
-    else if (prod && kb == 2 && vb == 3) e = launch_few_attend<2, 4, true, 4, 8>(qm, a, grid, stream);
-    else if (prod && kb == 1 && vb == 2) e = launch_few_attend<1, 2, true, 2, 4>(qm, a, grid, stream);
-    else if (!prod && kb == 4 && vb == 4) e = launch_few_attend<4, 16, false, 4, 16>(qm, a, grid, stream);
-    else if (!prod && kb == 3 && vb == 3) e = launch_few_attend<4, 8, false, 4, 8>(qm, a, grid, stream);
-    else if (!prod && kb == 2 && vb == 2) e = launch_few_attend<2, 4, false, 2, 4>(qm, a, grid, stream);
-    else return cudaErrorInvalidValue;
+    e = cudaErrorInvalidValue;
+#define TQ_FEW(P, KB, VB, ...)                                                                                  \
+    if (prod == P && kb == KB && vb == VB)                                                                       \
+        e = plan.rows == 32 ? launch_few_attend<32, __VA_ARGS__>(qm, a, grid, stream)                           \
+                            : launch_few_attend<128, __VA_ARGS__>(qm, a, grid, stream);
+    TQ_FEW(true, 3, 4, 4, 8, true, 4, 16)
+    TQ_FEW(true, 2, 3, 2, 4, true, 4, 8)
+    TQ_FEW(true, 1, 2, 1, 2, true, 2, 4)
+    TQ_FEW(false, 4, 4, 4, 16, false, 4, 16)
+    TQ_FEW(false, 3, 3, 4, 8, false, 4, 8)
+    TQ_FEW(false, 2, 2, 2, 4, false, 2, 4)
+#undef TQ_FEW
     if (e != cudaSuccess) return e;
-    count_launches(1);
 
     JoinArgs m{};
     m.part = a.part;
@@ -749,10 +831,7 @@ cudaError_t launch_chunk_few(const tq_ctx* ctx, const ChunkPlan& plan, const Chu
     e = cudaFuncSetAttribute(few_join_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kJoinSmem);
     if (e != cudaSuccess) return e;
     const long long blocks = (rows + kJoinRows - 1) / kJoinRows;
-    few_join_kernel<<<(unsigned)blocks, kJoinThreads, kJoinSmem, stream>>>(m);
-    e = cudaGetLastError();
-    if (e == cudaSuccess) count_launches(1);
-    return e;
+    return launch_after(few_join_kernel, dim3((unsigned)blocks), kJoinThreads, kJoinSmem, stream, m);
 }
 
 }  // namespace tq

@@ -176,6 +176,7 @@ cudaError_t launch_attend(const tq_ctx* ctx, const AttendCall& c, cudaStream_t s
 // A chunk call's way through its workspace (chunk.cu).
 struct ChunkPlan {
     bool few;            // few rows: straight over the packed pages (chunk_few.cu)
+    int rows;            // (query, head of a group) rows per CTA of the attention
     int kv_pad;          // tokens of a sequence, rounded up to whole tiles of 128
     int heads;           // kv heads decompressed at a time
     int splits;          // of the tokens, in the attention
