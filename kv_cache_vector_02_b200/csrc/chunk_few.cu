@@ -9,12 +9,12 @@
 // few_rotate_kernel   q' and s of every (query, head), fp16 (R^T as fp16 hi + lo)
 // few_attend_kernel   one CTA per (128 rows, kv head, split of the tokens); a row is a
 //                     (query, query head of the group) pair.  Per tile of 128 tokens:
-//   warps 4-11  two threads per token: its packed codes and signs (loaded a tile ahead)
+//   8 warps     two threads per token: its packed codes and signs (loaded a tile ahead)
 //               become fp16 levels and +-1 in registers, the values' times n_t/sqrt(d)
 //               (rounded to fp16, as decompressed values are), and go to swizzled
 //               operand tiles; a_t, b_t to shared memory
-//   warp 12     D1 = Q' C_k^T, D2 = S_q Sigma^T, O += P V on tcgen05
-//   warps 0-3   one thread per row: s = a_t D1 + b_t D2 (fp32; the score's two scalars are
+//   1 warp      D1 = Q' C_k^T, D2 = S_q Sigma^T, O += P V on tcgen05
+//   4 warps     one thread per row (32 rows at most: four per row): s = a_t D1 + b_t D2 (fp32; the score's two scalars are
 //               never rounded), mask, running maximum and sum, P to tensor memory.  Warps
 //               without a row only keep step.
 // few_join_kernel     the splits joined, o = R acc / l in fp32
@@ -38,7 +38,7 @@ using namespace sm100;
 constexpr int kFN = 128;                            // tokens of a tile
 constexpr uint32_t kFTile = 128 * kDim * 2, kFHalf = kFTile / 2;
 constexpr int kFThreads = 512;
-// Registers: 128 a thread at launch (the launch checks it), moved to the softmax.
+// Registers (ROWS = 128): 128 a thread at launch (the launch checks it), moved to the softmax.
 constexpr int kFRegs = 128, kFSoftmaxRegs = 208, kFCodeRegs = 112, kFIssueRegs = 80;
 static_assert(kFSoftmaxRegs + 2 * kFCodeRegs + kFIssueRegs == 4 * kFRegs, "the block's own registers");
 // Shared memory.  At most 32 rows (ROWS = 32): a 64-column block of Q' is 32 rows of 128 bytes,
@@ -53,7 +53,8 @@ struct FewSmem {
     static constexpr uint32_t kOffV = kOffK + 4 * kFTile;      // C_v n / sqrt(d)
     static constexpr uint32_t kOffScal = kOffV + kVBufs * kFTile;  // float [2][2][128]: a_t, b_t
     static constexpr uint32_t kOffBar = kOffScal + 2 * 2 * 128 * 4;
-    static constexpr uint32_t kBytes = kOffBar + 256;
+    static constexpr uint32_t kOffTop = kOffBar + 256;         // float [4][32] (ROWS = 32)
+    static constexpr uint32_t kBytes = kOffTop + (ROWS == 32 ? 512 : 0);
     static_assert(kBytes <= 232448, "shared memory budget");
     static_assert(kOffK % 1024 == 0 && kBlock % 1024 == 0, "swizzled tiles");
 };
@@ -107,6 +108,18 @@ __device__ __forceinline__ float few_max3(float x, float y, float z) {
     asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(m) : "f"(x), "f"(y), "f"(z));
     return m;
 }
+
+// Named barriers of n threads: whether x holds in any of them; plain.
+__device__ __forceinline__ bool any_of_threads(int id, int n, bool x) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %3, 0;\n\tbarrier.red.or.pred q, %1, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"(id), "r"(n), "r"((uint32_t)x)
+        : "memory");
+    return r != 0;
+}
+__device__ __forceinline__ void sync_threads(int id, int n) { asm volatile("barrier.sync %0, %1;" ::"r"(id), "r"(n) : "memory"); }
 
 // Half a row of packed codes of W bits: 8 W bytes.
 template <int W>
@@ -182,7 +195,13 @@ __global__ void __launch_bounds__(kFThreads, 1)
         for (int r = threadIdx.x; r < nrows; r += kFThreads) a.ml[prow0 + out_row(r)] = make_float2(-INFINITY, 0.f);
         return;
     }
-    const int live_warps = (nrows + 31) / 32;
+    // roles: with 32 rows four softmax warps, on the one lane quarter that has them, share a
+    // tile's tokens; with 128 one per quarter
+    constexpr int kParts = ROWS == 32 ? 4 : 1;
+    const bool softmax = ROWS == 32 ? warp % 4 == 0 : warp < 4;
+    const int coder = ROWS == 32 ? (warp % 4 == 0 ? -1 : (warp / 4) * 3 + warp % 4 - 1) : warp - 4;
+    constexpr int kWarpIssue = ROWS == 32 ? 11 : 12;  // (ROWS = 32: coder 8)
+    const int live_warps = ROWS == 32 ? kParts : (nrows + 31) / 32;
 
     const uint32_t bars = sbase + M::kOffBar;
     auto bar = [&](int i) -> uint32_t { return bars + 8u * (uint32_t)i; };
@@ -217,7 +236,7 @@ __global__ void __launch_bounds__(kFThreads, 1)
         for (int x = 0; x < (PROD ? 4 : 2); ++x)
             tma_load_3d(sbase + M::kOffQ + x * M::kBlock, &q_map, 64 * x, hk * a.G, c0 + q0, bar(kFBQ));
     }
-    if (warp == 12) {
+    if (warp == kWarpIssue) {
         tmem_alloc(smem_u32(tmem_slot), 512);
         tmem_relinquish();
     }
@@ -226,10 +245,10 @@ __global__ void __launch_bounds__(kFThreads, 1)
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
 
-    if (warp >= 4 && warp < 12) {
-        set_registers_down<kFCodeRegs>();
+    if (!softmax && coder < 8) {
+        if (ROWS != 32) set_registers_down<kFCodeRegs>();
         // ------------------------------------------------------------ codes to operands
-        const int tok = threadIdx.x & 127, half = warp >= 8 ? 1 : 0, r16 = tok % kPage;
+        const int tok = (coder & 3) * 32 + lane, half = coder >> 2, r16 = tok % kPage;
         const uint32_t lead = lane == 0;
         struct Raw {  // a tile's packed bytes of this thread's half token
             HalfRow<WK> kw;
@@ -238,17 +257,19 @@ __global__ void __launch_bounds__(kFThreads, 1)
             float kn, kg, vn;
             bool bad;
         };
-        // block of the thread's token in tile j: -1 behind the last token, -2 out of range
+        // block of the thread's token in tile j (nothing looks at it before fetch does)
+        const int32_t* table = a.block_table + (size_t)b * a.max_blocks;
+        auto here = [&](int j) { return j < n && (j0 + j) * kFN + tok < kv_len; };
         auto block_of = [&](int j) -> int {
-            const int t = (j0 + j) * kFN + tok;
-            if (j >= n || t >= kv_len) return -1;
-            const int blk = a.block_table[(size_t)b * a.max_blocks + t / kPage];
-            return blk >= 0 && blk < a.num_blocks ? blk : -2;
+            int blk = 0;
+            if (here(j)) blk = table[((j0 + j) * kFN + tok) / kPage];
+            return blk;
         };
-        auto fetch = [&](Raw& r, int blk) {
+        auto fetch = [&](Raw& r, int j, int blk) {
             r.kn = r.kg = r.vn = 0.f;
-            r.bad = blk == -2;
-            if (blk < 0) return;
+            r.bad = blk < 0 || blk >= a.num_blocks;
+            if (!here(j)) r.bad = false;
+            else if (!r.bad) {
             const uint8_t* kp = a.kc + ((size_t)blk * a.Hkv + hk) * a.lk.bytes;
             const uint8_t* vp = a.vc + ((size_t)blk * a.Hkv + hk) * a.lv.bytes;
             r.kw.load(kp + r16 * a.lk.code_row + half * 8 * WK);
@@ -257,6 +278,7 @@ __global__ void __launch_bounds__(kFThreads, 1)
             r.kn = reinterpret_cast<const float*>(kp + a.lk.norm_off)[r16];
             if (PROD) r.kg = reinterpret_cast<const float*>(kp + a.lk.gamma_off)[r16];
             r.vn = reinterpret_cast<const float*>(vp + a.lv.norm_off)[r16];
+            }
         };
         const uint32_t row = (uint32_t)tok * 128 + half * kFHalf;
         bool ok = true;
@@ -320,22 +342,22 @@ __global__ void __launch_bounds__(kFThreads, 1)
         Raw r0{}, r1{};
         int blk = block_of(0);
         int next = block_of(1);
-        fetch(r0, blk);
+        fetch(r0, 0, blk);
         blk = block_of(2);
-        fetch(r1, next);
+        fetch(r1, 1, next);
 #pragma unroll 1
         for (int j = 0; j < n && ok; j += 2) {
             next = block_of(j + 3);
             tile(r0, j, 0);
-            fetch(r0, blk);
+            fetch(r0, j + 2, blk);
             if (j + 1 >= n || !ok) break;
             blk = block_of(j + 4);
             tile(r1, j + 1, 1);
-            fetch(r1, next);
+            fetch(r1, j + 3, next);
         }
-    } else if (warp >= 12) {
-        set_registers_down<kFIssueRegs>();
-        if (warp == 12) {
+    } else if (!softmax) {
+        if (ROWS != 32) set_registers_down<kFIssueRegs>();
+        if (warp == kWarpIssue) {
         // ------------------------------------------------------------ MMA issuer (converged warp)
         constexpr uint32_t id_s = idesc_f16(128, kFN), id_o = idesc_f16(128, kDim) | (1u << 16);
         const uint32_t lead = elect_lane();
@@ -396,31 +418,35 @@ __global__ void __launch_bounds__(kFThreads, 1)
         __syncwarp();
         }
     } else {
-        set_registers_up<kFSoftmaxRegs>();
-        if (warp < live_warps) {
+        if (ROWS != 32) set_registers_up<kFSoftmaxRegs>();
+        if (ROWS == 32 || warp < live_warps) {
         // ------------------------------------------------------------ softmax
-        const int row = threadIdx.x;
-        const uint32_t lanes = (uint32_t)warp << 21, lead = lane == 0;
-        const uint32_t ts = tmem + lanes, tp = tmem + kFColP + lanes, to = tmem + kFColO + lanes;
+        constexpr int kCols = kFN / kParts, kChunks = kCols / 32;  // tokens of this thread
+        const int part = ROWS == 32 ? warp / 4 : 0, row = ROWS == 32 ? lane : (int)threadIdx.x;
+        const uint32_t lanes = ROWS == 32 ? 0u : (uint32_t)warp << 21, lead = lane == 0;
+        const uint32_t ts = tmem + lanes + kCols * part, tp = tmem + kFColP + kCols / 2 * part + lanes;
+        const uint32_t to = tmem + kFColO + kCols * part + lanes;
         const bool live = row < nrows;
         const int limit = live ? off + q0 + row / a.G - j0 * kFN : -1;  // its last token, from the split's first
         const int masked_from = (off + q0 + 1) / kFN - j0;             // first tile with a masked pair
+        float* tops = reinterpret_cast<float*>(smem + M::kOffTop) + lane;  // [kParts][32]
         float m = -INFINITY;
         float2 sum[2] = {{0.f, 0.f}, {0.f, 0.f}};
         bool ok = true;
-        auto wait = [&](int x, int phase) -> bool {
-            if (mbar_wait_all(bar(x), (uint32_t)phase & 1u, abort, kFWaitNs)) return true;
-            give_up();
-            return false;
+        // after a wait that gave up the loop goes on without waiting: the parts' barriers need every warp
+        auto wait = [&](int x, int phase) {
+            if (ok && !mbar_wait_all(bar(x), (uint32_t)phase & 1u, abort, kFWaitNs)) {
+                give_up();
+                ok = false;
+            }
         };
         for (int j = 0; j < n; ++j) {
-            ok = wait(kFBS, j);
-            if (!ok) break;
+            wait(kFBS, j);
             tc_fence_after();
-            uint32_t s[4][32];
-            const float4* sc = reinterpret_cast<const float4*>(smem + M::kOffScal + (j & 1) * 1024);
+            uint32_t s[kChunks][32];
+            const float4* sc = reinterpret_cast<const float4*>(smem + M::kOffScal + (j & 1) * 1024) + kCols / 4 * part;
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
+            for (int q = 0; q < kChunks; ++q) {
                 uint32_t d2[32];
                 tmem_ld32(ts + 32 * q, s[q]);
                 if (PROD) tmem_ld32(ts + kFColS2 + 32 * q, d2);
@@ -448,45 +474,58 @@ __global__ void __launch_bounds__(kFThreads, 1)
             mbar_arrive_lead(lead, bar(kFBL));
             mbar_arrive_lead(lead, bar(kFBKEmpty + (j & 1)));
             if (j >= masked_from) {
-                const int lim = limit - j * kFN;
+                const int lim = limit - j * kFN - kCols * part;
 #pragma unroll
-                for (int q = 0; q < 4; ++q)
+                for (int q = 0; q < kChunks; ++q)
 #pragma unroll
                     for (int e = 0; e < 32; ++e)
                         if (32 * q + e > lim) s[q][e] = 0xFF800000u;  // -inf
             }
             if (pb.x | pb.y) {
 #pragma unroll
-                for (int q = 0; q < 4; ++q)
+                for (int q = 0; q < kChunks; ++q) {
+                    const int page = 2 * (kChunks * part + q);  // the chunk's first of the tile's eight
+                    const uint32_t w = (page < 4 ? pb.x : pb.y) >> (8 * (page & 3));
 #pragma unroll
                     for (int e = 0; e < 32; ++e)
-                        if (((q < 2 ? pb.x : pb.y) >> (8 * (2 * (q & 1) + e / 16))) & 1u) s[q][e] = 0xFF800000u;
+                        if ((w >> (8 * (e / 16))) & 1u) s[q][e] = 0xFF800000u;
+                }
             }
-            float mx[4];
+            float top = -INFINITY;
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                mx[q] = few_max3(__uint_as_float(s[q][0]), __uint_as_float(s[q][1]), __uint_as_float(s[q][2]));
+            for (int q = 0; q < kChunks; ++q) {
+                float m0 = few_max3(__uint_as_float(s[q][0]), __uint_as_float(s[q][1]), __uint_as_float(s[q][2]));
+                float m1 = few_max3(__uint_as_float(s[q][16]), __uint_as_float(s[q][17]), __uint_as_float(s[q][18]));
 #pragma unroll
-                for (int e = 3; e < 31; e += 2)
-                    mx[q] = few_max3(mx[q], __uint_as_float(s[q][e]), __uint_as_float(s[q][e + 1]));
-                mx[q] = few_max3(mx[q], mx[q], __uint_as_float(s[q][31]));
+                for (int e = 3; e < 15; e += 2) {
+                    m0 = few_max3(m0, __uint_as_float(s[q][e]), __uint_as_float(s[q][e + 1]));
+                    m1 = few_max3(m1, __uint_as_float(s[q][16 + e]), __uint_as_float(s[q][17 + e]));
+                }
+                top = few_max3(top, few_max3(m0, m0, __uint_as_float(s[q][15])), few_max3(m1, m1, __uint_as_float(s[q][31])));
             }
-            float top = few_max3(few_max3(mx[0], mx[1], mx[2]), mx[3], mx[3]);
             // a NaN or infinite score makes the row's sum and outputs NaN; the maximum carries it
             if (!(top < INFINITY)) top = NAN;
-            const bool grow = top > m + kFRescale || (m == -INFINITY && top > m) || (top != top && m == m);
-            // the tile before is in O, and its P has been read
-            if (j > 0) ok = wait(kFBO, j - 1);
-            if (!ok) break;
-            if (__any_sync(0xffffffffu, grow)) {
+            auto grows = [&](float t) { return t > m + kFRescale || (m == -INFINITY && t > m) || (t != t && m == m); };
+            bool any = grows(top);
+            any = kParts > 1 ? any_of_threads(1, 32 * kParts, any) : __any_sync(0xffffffffu, any) != 0;
+            if (any) {
+                if (kParts > 1) {
+                    tops[32 * part] = top;
+                    sync_threads(1, 32 * kParts);
+#pragma unroll
+                    for (int i = 0; i < kParts; ++i) top = few_max3(top, top, tops[32 * i]);
+                    sync_threads(1, 32 * kParts);
+                }
+                const bool grow = grows(top);
                 const float mn = grow ? top : m;
                 if (j > 0) {
                     const float f = grow ? few_ex2(m - mn) : 1.f;  // (first maximum: ex2(-inf) = 0)
 #pragma unroll
                     for (int q = 0; q < 2; ++q) sum[q] = __fmul2_rn(sum[q], make_float2(f, f));
+                    wait(kFBO, j - 1);  // the tile before is in O
                     tc_fence_after();
 #pragma unroll 1
-                    for (int q = 0; q < 8; ++q) {
+                    for (int q = 0; q < 2 * kChunks; ++q) {
                         uint32_t o[16];
                         tmem_ld16(to + 16 * q, o);
                         tmem_ld_wait();
@@ -504,9 +543,9 @@ __global__ void __launch_bounds__(kFThreads, 1)
             }
             const float mm = m == -INFINITY ? 0.f : m;
             const float2 nm = make_float2(-mm, -mm);
+            uint32_t p[2 * kChunks][8];
 #pragma unroll
-            for (int q = 0; q < 8; ++q) {
-                uint32_t p[8];
+            for (int q = 0; q < 2 * kChunks; ++q) {
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
                     const int i = 16 * q + 2 * e;
@@ -516,30 +555,40 @@ __global__ void __launch_bounds__(kFThreads, 1)
                     x.y = few_ex2(x.y);
                     sum[e & 1] = __fadd2_rn(sum[e & 1], x);
                     const __half2 hp = __floats2half2_rn(x.x, x.y);
-                    p[e] = *reinterpret_cast<const uint32_t*>(&hp);
+                    p[q][e] = *reinterpret_cast<const uint32_t*>(&hp);
                 }
-                tmem_st8(tp + 8 * q, p);
             }
+            // the tile before's P has been read
+            if (j > 0 && !any) wait(kFBO, j - 1);
+#pragma unroll
+            for (int q = 0; q < 2 * kChunks; ++q) tmem_st8(tp + 8 * q, p[q]);
             tmem_st_wait();
             tc_fence_before();
             mbar_arrive_lead(lead, bar(kFBP));
         }
-        if (ok) ok = wait(kFBO, n - 1);
-        const float l = (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+        wait(kFBO, n - 1);
+        float l = (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+        if (kParts > 1) {  // the row's sum: the same terms in the same order in every part
+            tops[32 * part] = l;
+            sync_threads(1, 32 * kParts);
+            l = 0.f;
+#pragma unroll
+            for (int i = 0; i < kParts; ++i) l += tops[32 * i];
+        }
         const size_t prow = live ? prow0 + out_row(row) : 0;
-        if (live) {
+        if (live && part == 0) {
             const bool hit = limit + j0 * kFN >= *reinterpret_cast<volatile int*>(first_bad);
             a.ml[prow] = ok ? make_float2(m, hit ? NAN : l) : make_float2(-INFINITY, 0.f);
         }
         if (ok) {
             tc_fence_after();
 #pragma unroll 1
-            for (int q = 0; q < 4; ++q) {
+            for (int q = 0; q < kChunks; ++q) {
                 uint32_t o[32];
                 tmem_ld32(to + 32 * q, o);
                 tmem_ld_wait();
                 if (!live) continue;
-                float4* d = reinterpret_cast<float4*>(a.part + prow * kDim + 32 * q);
+                float4* d = reinterpret_cast<float4*>(a.part + prow * kDim + kCols * part + 32 * q);
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
                     d[i] = make_float4(__uint_as_float(o[4 * i]), __uint_as_float(o[4 * i + 1]),
@@ -550,7 +599,7 @@ __global__ void __launch_bounds__(kFThreads, 1)
         }
     }
     __syncthreads();
-    if (warp == 12) {
+    if (warp == kWarpIssue) {
         tc_fence_after();
         tmem_dealloc(tmem, 512);
     }
@@ -746,7 +795,7 @@ cudaError_t launch_few_attend(const CUtensorMap& q, const FewArgs& a, dim3 grid,
     cudaFuncAttributes attr{};
     cudaError_t e = cudaFuncGetAttributes(&attr, k);
     if (e != cudaSuccess) return e;
-    if (attr.numRegs != kFRegs) return cudaErrorInvalidConfiguration;  // the register split would not add up
+    if (ROWS != 32 && attr.numRegs != kFRegs) return cudaErrorInvalidConfiguration;  // the split would not add up
     e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)FewSmem<ROWS>::kBytes);
     if (e != cudaSuccess) return e;
     return launch_after(k, grid, kFThreads, FewSmem<ROWS>::kBytes, stream, q, a);
