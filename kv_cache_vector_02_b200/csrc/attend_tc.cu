@@ -578,11 +578,8 @@ cudaError_t launch_attend(const tq_ctx* ctx, const AttendCall& c, cudaStream_t s
         !encode_heads_tmap(&mk, c.k, c.heads, kv_rows, c.k_stride, 1, kAN) ||
         !encode_heads_tmap(&mv, c.v, c.heads, kv_rows, c.v_stride, 1, kAN))
         return cudaErrorInvalidValue;
-    cudaFuncAttributes attr{};
-    cudaError_t e = cudaFuncGetAttributes(&attr, attend_tc_kernel);
-    if (e != cudaSuccess) return e;
-    if (attr.numRegs != kARegs) return cudaErrorInvalidConfiguration;  // the register split would not add up
-    e = cudaFuncSetAttribute(attend_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kASmem);
+    static std::atomic<uint64_t> ready{0};
+    cudaError_t e = ready_kernel(attend_tc_kernel, ready, (int)kASmem, kARegs);  // (the register split has to add up)
     if (e != cudaSuccess) return e;
     // slots of all sequences: floor(total / q) + B bounds every sequence's last one
     const long long slots = (long long)c.total_q / (2 * a.QT) + c.B;

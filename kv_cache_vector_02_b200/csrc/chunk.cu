@@ -405,7 +405,8 @@ template <int WK, int LK, bool PROD, int WV, int LV>
 cudaError_t launch_unpack(const tq_ctx* ctx, const CUtensorMap& ko, const CUtensorMap& vo, const UnpackArgs& a,
                           cudaStream_t stream) {
     auto k = unpack_tc_kernel<WK, LK, PROD, WV, LV>;
-    const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kUSmem);
+    static std::atomic<uint64_t> ready{0};
+    const cudaError_t e = ready_kernel(k, ready, (int)kUSmem);
     if (e != cudaSuccess) return e;
     const long long items = (long long)a.B * a.tiles * a.heads;
     const unsigned grid = (unsigned)(items < ctx->sm_count ? items : ctx->sm_count);

@@ -792,11 +792,8 @@ cudaError_t launch_after(void (*k)(P...), dim3 grid, int threads, uint32_t smem,
 template <int ROWS, int WK, int LK, bool PROD, int WV, int LV>
 cudaError_t launch_few_attend(const CUtensorMap& q, const FewArgs& a, dim3 grid, cudaStream_t stream) {
     auto k = few_attend_kernel<ROWS, WK, LK, PROD, WV, LV>;
-    cudaFuncAttributes attr{};
-    cudaError_t e = cudaFuncGetAttributes(&attr, k);
-    if (e != cudaSuccess) return e;
-    if (ROWS != 32 && attr.numRegs != kFRegs) return cudaErrorInvalidConfiguration;  // the split would not add up
-    e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)FewSmem<ROWS>::kBytes);
+    static std::atomic<uint64_t> ready{0};
+    const cudaError_t e = ready_kernel(k, ready, (int)FewSmem<ROWS>::kBytes, ROWS == 32 ? 0 : kFRegs);  // (the split has to add up)
     if (e != cudaSuccess) return e;
     return launch_after(k, grid, kFThreads, FewSmem<ROWS>::kBytes, stream, q, a);
 }
@@ -877,7 +874,8 @@ cudaError_t launch_chunk_few(const tq_ctx* ctx, const ChunkPlan& plan, const Chu
     m.RT = ctx->dev.RT;
     m.out = c.out;
     m.out_fp32 = c.out_fp32;
-    e = cudaFuncSetAttribute(few_join_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kJoinSmem);
+    static std::atomic<uint64_t> ready{0};
+    e = ready_kernel(few_join_kernel, ready, (int)kJoinSmem);
     if (e != cudaSuccess) return e;
     const long long blocks = (rows + kJoinRows - 1) / kJoinRows;
     return launch_after(few_join_kernel, dim3((unsigned)blocks), kJoinThreads, kJoinSmem, stream, m);

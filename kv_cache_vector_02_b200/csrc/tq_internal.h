@@ -102,6 +102,24 @@ void count_launches(unsigned n);
 // copies so that its bounded waits run out (tq_debug_stall).
 bool take_stall(const tq_ctx* ctx);
 
+// Sets kernel k up for `smem` bytes of dynamic shared memory, once per device (`done` is the
+// kernel's own bit per device), and refuses it if `regs` is not 0 and not what the kernel was
+// built with (one that moves its registers between warps relies on their number).
+template <typename K>
+cudaError_t ready_kernel(K k, std::atomic<uint64_t>& done, int smem, int regs = 0) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev >= 0 && dev < 64 && ((done.load(std::memory_order_relaxed) >> dev) & 1u)) return cudaSuccess;
+    cudaFuncAttributes attr{};
+    e = cudaFuncGetAttributes(&attr, k);
+    if (e != cudaSuccess) return e;
+    if (regs && attr.numRegs != regs) return cudaErrorInvalidConfiguration;
+    e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e == cudaSuccess && dev >= 0 && dev < 64) done.fetch_or(uint64_t(1) << dev, std::memory_order_relaxed);
+    return e;
+}
+
 // Kernel launchers (CUDA translation units).  Each returns cudaSuccess or the
 // launch error.
 cudaError_t launch_compress_tc(const tq_ctx* ctx, int kind, const uint16_t* x, int T, int H, const int32_t* slots,

@@ -308,30 +308,34 @@ def _token_stride(t, what: str, name: str) -> int:
     """Elements from one token of a [T, H, 128] fp16 tensor to the next; its heads must lie
     side by side (a view into a fused projection may have a longer stride)."""
     import torch
-    T, H, d = t.shape if t.dim() == 3 else (0, 0, 0)
-    ok = t.dim() == 3 and d == 128 and t.dtype is torch.float16 and H > 0
-    if ok and T > 0:
-        st = t.stride()
-        ok = st[2] == 1 and (H == 1 or st[1] == 128) and (T == 1 or (st[0] >= 128 * H and st[0] % 8 == 0))
-    if not ok:
-        raise TQError(TQ_ERR_INVALID_ARG, "%s: %s must be [T, H, 128] of %s, each token's heads contiguous, got %s %s "
-                      "with strides %s" % (what, name, torch.float16, tuple(t.shape), t.dtype, tuple(t.stride())))
-    return t.stride(0) if T > 1 else 128 * H
+    if t.dim() == 3 and t.dtype is torch.float16:
+        T, H, d = t.shape
+        s0, s1, s2 = t.stride()
+        if d == 128 and H > 0 and (T == 0 or (s2 == 1 and (H == 1 or s1 == 128) and
+                                              (T == 1 or (s0 >= 128 * H and s0 % 8 == 0)))):
+            return s0 if T > 1 else 128 * H
+    raise TQError(TQ_ERR_INVALID_ARG, "%s: %s must be [T, H, 128] of %s, each token's heads contiguous, got %s %s "
+                  "with strides %s" % (what, name, torch.float16, tuple(t.shape), t.dtype, tuple(t.stride())))
 
 
-def _same_device(what: str, first, *others):
-    """Every tensor on one device; the stream of that device's current stream by default."""
+def _same_device(what: str, first, *others) -> int:
+    """The device index (-1: the host) that every tensor is on."""
+    dev = first.get_device()
     for t in others:
-        if t is not None and t.device != first.device:
+        if t is not None and t.get_device() != dev:
             raise TQError(TQ_ERR_INVALID_ARG, "%s: tensors on %s and %s must be on one device" % (
                 what, first.device, t.device))
+    return dev
 
 
-def _stream_on(stream, t) -> int:
-    if stream is None and t.is_cuda:
-        import torch
-        return torch.cuda.current_stream(t.device).cuda_stream
-    return 0 if stream is None else _stream(stream)
+def _stream_on(stream, dev: int) -> int:
+    """The stream's handle; by default the current stream of device `dev`."""
+    if stream is not None:
+        return _stream(stream)
+    if dev < 0:
+        return 0
+    import torch
+    return torch.cuda.current_stream(dev).cuda_stream
 
 
 def tq_rope_plan(rot_dim: int = 128, layout: int = ROPE_HALF, base: float = 10000.0, scaling: int = ROPE_SCALE_NONE,
@@ -352,30 +356,28 @@ def tq_rope(table: RopeTable, q, k, positions, q_out=None, k_out=None, transpose
     ref = q if q is not None else k
     if ref is None:
         raise TQError(TQ_ERR_INVALID_ARG, "tq_rope: no input")
-    T = int(ref.shape[0])
-    args, heads = [], []
-    for x, o, n in ((q, q_out, "q"), (k, k_out, "k")):
-        if x is None:
-            if o is not None:
-                raise TQError(TQ_ERR_INVALID_ARG, "%s: %s_out without %s" % (what, n, n))
-            args.append((None, 0, None, 0))
-            heads.append(0)
-            continue
-        o = x if o is None else o
-        sx, so = _token_stride(x, what, n), _token_stride(o, what, n + "_out")
-        if x.shape[0] != T or o.shape != x.shape:
-            raise TQError(TQ_ERR_INVALID_ARG, "%s: %s and its output must be of one shape, with as many tokens as the "
-                          "other input" % (what, n))
-        args.append((x, sx, o, so))
-        heads.append(int(x.shape[1]))
+    T = ref.shape[0]
+    sq = sk = sqo = sko = Hq = Hkv = 0
+    if q is not None:
+        q_out = q if q_out is None else q_out
+        sq, sqo, Hq = _token_stride(q, what, "q"), _token_stride(q_out, what, "q_out"), q.shape[1]
+        if q_out is not q and q_out.shape != q.shape:
+            raise TQError(TQ_ERR_INVALID_ARG, "%s: q and q_out must be of one shape" % what)
+    elif q_out is not None:
+        raise TQError(TQ_ERR_INVALID_ARG, "%s: q_out without q" % what)
+    if k is not None:
+        k_out = k if k_out is None else k_out
+        sk, sko, Hkv = _token_stride(k, what, "k"), _token_stride(k_out, what, "k_out"), k.shape[1]
+        if k.shape[0] != T or (k_out is not k and k_out.shape != k.shape):
+            raise TQError(TQ_ERR_INVALID_ARG, "%s: k and k_out must be of one shape, with q's tokens" % what)
+    elif k_out is not None:
+        raise TQError(TQ_ERR_INVALID_ARG, "%s: k_out without k" % what)
     _expect(positions, (T,), (torch.int32,), what, "positions")
-    (q, sq, qo, sqo), (k, sk, ko, sko) = args
-    _same_device(what, ref, q, k, qo, ko, positions)
-    s = _stream_on(stream, ref)
-    call = (ctypes.byref(table), _ptr(q), sq, _ptr(k), sk, T, heads[0], heads[1], _ptr(positions), _ptr(qo), sqo,
-            _ptr(ko), sko, 1 if transpose else 0, s)
-    if ref.is_cuda and ref.device.index != torch.cuda.current_device():
-        with torch.cuda.device(ref.device):
+    dev = _same_device(what, ref, k, q_out, k_out, positions)
+    call = (table, _ptr(q), sq, _ptr(k), sk, T, Hq, Hkv, positions.data_ptr(), _ptr(q_out), sqo, _ptr(k_out), sko,
+            1 if transpose else 0, _stream_on(stream, dev))
+    if dev >= 0 and dev != torch.cuda.current_device():
+        with torch.cuda.device(dev):
             _check(_lib.tq_rope(*call), what)
     else:
         _check(_lib.tq_rope(*call), what)
@@ -388,18 +390,18 @@ def tq_prompt_attention(ctx: Context, q, k, v, cu_seqlens, out, scale: float = 0
     import torch
     what = "tq_prompt_attention"
     sq, sk, sv = _token_stride(q, what, "q"), _token_stride(k, what, "k"), _token_stride(v, what, "v")
-    T, Hq, Hkv = int(q.shape[0]), int(q.shape[1]), int(k.shape[1])
+    (T, Hq, _), Hkv = q.shape, k.shape[1]
     if k.shape[0] != T or v.shape != k.shape:
         raise TQError(TQ_ERR_INVALID_ARG, "%s: k and v must be of one shape, with q's tokens" % what)
     _expect(cu_seqlens, (None,), (torch.int32,), what, "cu_seqlens")
-    B = int(cu_seqlens.shape[0]) - 1
+    B = cu_seqlens.shape[0] - 1
     if B < 0:
         raise TQError(TQ_ERR_INVALID_ARG, "%s: cu_seqlens must have B + 1 entries" % what)
     _expect(out, (T, Hq, 128), (torch.float16, torch.float32), what, "out")
-    _same_device(what, q, k, v, cu_seqlens, out)
-    _check(_lib.tq_prompt_attention(ctx.handle, _ptr(q), sq, _ptr(k), sk, _ptr(v), sv, T, _ptr(cu_seqlens), B, Hq, Hkv,
-                                    float(scale), _ptr(out), 1 if out.dtype == torch.float32 else 0,
-                                    _stream_on(stream, q)), what)
+    dev = _same_device(what, q, k, v, cu_seqlens, out)
+    _check(_lib.tq_prompt_attention(ctx.handle, q.data_ptr(), sq, k.data_ptr(), sk, v.data_ptr(), sv, T,
+                                    cu_seqlens.data_ptr(), B, Hq, Hkv, scale, out.data_ptr(),
+                                    1 if out.dtype is torch.float32 else 0, _stream_on(stream, dev)), what)
 
 
 def tq_chunk_workspace_bytes(ctx: Context, B: int, total_q: int, Hq: int, Hkv: int, max_seq_len: int) -> int:
@@ -417,23 +419,24 @@ def tq_chunk_attention(ctx: Context, q, cu_q, k_cache, v_cache, block_table, seq
     tensor of tq_chunk_workspace_bytes (see tq.h)."""
     import torch
     what = "tq_chunk_attention"
-    total_q, Hq = int(q.shape[0]), int(q.shape[1])
+    total_q, Hq = q.shape[0], q.shape[1]
     if Hkv is None:
-        Hkv = int(k_cache.shape[1])
+        Hkv = k_cache.shape[1]
     _expect(q, (total_q, Hq, ctx.head_dim), (torch.float16,), what, "q")
     _expect(k_cache, (None, Hkv, tq_chunk_bytes(ctx, KIND_KEY)), (torch.uint8,), what, "k_cache")
     _expect(v_cache, (int(k_cache.shape[0]), Hkv, tq_chunk_bytes(ctx, KIND_VALUE)), (torch.uint8,), what, "v_cache")
     _expect(seq_lens, (None,), (torch.int32,), what, "seq_lens")
-    B = int(seq_lens.shape[0])
+    B = seq_lens.shape[0]
     _expect(block_table, (B, None), (torch.int32,), what, "block_table")
     _expect(cu_q, (B + 1,), (torch.int32,), what, "cu_q")
     _expect(out, (total_q, Hq, ctx.head_dim), (torch.float16, torch.float32), what, "out")
     _expect(workspace, (None,), (torch.uint8,), what, "workspace")
-    _same_device(what, q, cu_q, k_cache, v_cache, block_table, seq_lens, out, workspace)
-    _check(_lib.tq_chunk_attention(ctx.handle, _ptr(q), _ptr(cu_q), _ptr(k_cache), _ptr(v_cache), int(k_cache.shape[0]),
-                                   _ptr(block_table), int(block_table.shape[1]), _ptr(seq_lens), B, total_q, Hq, Hkv,
-                                   int(max_seq_len), float(scale), _ptr(out), 1 if out.dtype == torch.float32 else 0,
-                                   _ptr(workspace), int(workspace.numel()), _stream_on(stream, q)), what)
+    dev = _same_device(what, q, cu_q, k_cache, v_cache, block_table, seq_lens, out, workspace)
+    _check(_lib.tq_chunk_attention(ctx.handle, q.data_ptr(), cu_q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+                                   k_cache.shape[0], block_table.data_ptr(), block_table.shape[1], seq_lens.data_ptr(),
+                                   B, total_q, Hq, Hkv, max_seq_len, scale, out.data_ptr(),
+                                   1 if out.dtype is torch.float32 else 0, workspace.data_ptr(), workspace.numel(),
+                                   _stream_on(stream, dev)), what)
 
 
 NOALLOC_SCRATCH_BYTES = 8 << 20
