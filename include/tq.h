@@ -383,6 +383,7 @@ TQ_API size_t tq_chunk_workspace_bytes(const tq_ctx* ctx, int B, int total_q, in
  *   q_dev          : [total_q][Hq][128] fp16, device, 16-byte aligned; Hq / Hkv 1 .. 128.
  *   cu_q_dev       : [B + 1] int32, non-decreasing, 0 .. total_q; as tq_prompt_attention's
  *                    cu_seqlens.  n_b = 0 is allowed.
+ *   num_blocks     : blocks of the caches, at least 1 (TQ_ERR_INVALID_ARG otherwise).
  *   block_table_dev: [B][max_blocks] int32.  A block id outside [0, num_blocks) skips the
  *                    page and sets TQ_DEVERR_BLOCK.
  *   seq_lens_dev   : [B] int32, n_b <= L_b <= max_seq_len and <= max_blocks*16 (else the

@@ -9,7 +9,7 @@
 // few_rotate_kernel   q' and s of every (query, head), fp16 (R^T as fp16 hi + lo)
 // few_attend_kernel   one CTA per (128 rows, kv head, split of the tokens); a row is a
 //                     (query, query head of the group) pair.  Per tile of 128 tokens:
-//   8 warps     two threads per token: its packed codes and signs (loaded a tile ahead)
+//   8 warps     two threads per token (32 rows at most: 16 warps, four): its packed codes and signs (loaded a tile ahead)
 //               become fp16 levels and +-1 in registers, the values' times n_t/sqrt(d)
 //               (rounded to fp16, as decompressed values are), and go to swizzled
 //               operand tiles; a_t, b_t to shared memory
@@ -37,7 +37,6 @@ using namespace sm100;
 
 constexpr int kFN = 128;                            // tokens of a tile
 constexpr uint32_t kFTile = 128 * kDim * 2, kFHalf = kFTile / 2;
-constexpr int kFThreads = 512;
 // Registers (ROWS = 128): 128 a thread at launch (the launch checks it), moved to the softmax.
 constexpr int kFRegs = 128, kFSoftmaxRegs = 208, kFCodeRegs = 112, kFIssueRegs = 80;
 static_assert(kFSoftmaxRegs + 2 * kFCodeRegs + kFIssueRegs == 4 * kFRegs, "the block's own registers");
@@ -47,6 +46,8 @@ static_assert(kFSoftmaxRegs + 2 * kFCodeRegs + kFIssueRegs == 4 * kFRegs, "the b
 template <int ROWS>
 struct FewSmem {
     static constexpr int kVBufs = ROWS == 32 ? 2 : 1;
+    static constexpr int kSub = ROWS == 32 ? 4 : 2;            // threads per token that decode it
+    static constexpr int kThreads = ROWS == 32 ? 768 : 512;
     static constexpr uint32_t kBlock = ROWS * 128;             // 64 columns of Q'
     static constexpr uint32_t kOffQ = 0;                       // q' | s: two blocks each
     static constexpr uint32_t kOffK = 4 * kBlock;              // two buffers of C_k | Sigma
@@ -109,6 +110,25 @@ __device__ __forceinline__ float few_max3(float x, float y, float z) {
     return m;
 }
 
+// 2^x of a pair on the FMA pipe: n = round(x) by adding 1.5 * 2^23 (its low bits are n), f = x - n
+// in [-1/2, 1/2], 2^f by the polynomial of degree 4 with the smallest relative error there
+// (Remez exchange: 2.7e-6, far below P's rounding to fp16), and n added to the exponent.
+// Below -126 the result is 2^-126, which is 0 in fp16.  A NaN gives some number.
+__device__ __forceinline__ float2 few_ex2_poly(float2 x) {
+    const float2 magic = make_float2(12582912.f, 12582912.f), minus = make_float2(-12582912.f, -12582912.f);
+    x.x = fmaxf(x.x, -126.f);
+    x.y = fmaxf(x.y, -126.f);
+    const float2 t = __fadd2_rn(x, magic), r = __fadd2_rn(t, minus);
+    const float2 f = __ffma2_rn(r, make_float2(-1.f, -1.f), x);
+    float2 p = __ffma2_rn(f, make_float2(0.009570102207362652f, 0.009570102207362652f),
+                          make_float2(0.05591785907745361f, 0.05591785907745361f));
+    p = __ffma2_rn(p, f, make_float2(0.240247443318367f, 0.240247443318367f));
+    p = __ffma2_rn(p, f, make_float2(0.6931217908859253f, 0.6931217908859253f));
+    p = __ffma2_rn(p, f, make_float2(0.9999992847442627f, 0.9999992847442627f));
+    return make_float2(__int_as_float(__float_as_int(p.x) + (__float_as_int(t.x) << 23)),
+                       __int_as_float(__float_as_int(p.y) + (__float_as_int(t.y) << 23)));
+}
+
 // Named barriers of n threads: whether x holds in any of them; plain.
 __device__ __forceinline__ bool any_of_threads(int id, int n, bool x) {
     uint32_t r;
@@ -121,35 +141,50 @@ __device__ __forceinline__ bool any_of_threads(int id, int n, bool x) {
 }
 __device__ __forceinline__ void sync_threads(int id, int n) { asm volatile("barrier.sync %0, %1;" ::"r"(id), "r"(n) : "memory"); }
 
-// Half a row of packed codes of W bits: 8 W bytes.
-template <int W>
-struct HalfRow {
-    uint32_t w[2 * W];
+// One of SUB equal parts of a row of packed codes of W bits: 16 W / SUB bytes.
+template <int W, int SUB>
+struct PartRow {
+    static constexpr int kWords = 4 * W / SUB;
+    uint32_t w[kWords];
     __device__ __forceinline__ void load(const uint8_t* p) {
-        if (W == 4) {
+        if (kWords % 4 == 0) {
 #pragma unroll
-            for (int i = 0; i < W / 2; ++i) {
-                const uint4 x = *reinterpret_cast<const uint4*>(p + 16 * i);
+            for (int i = 0; i < kWords / 4; ++i) {
+                const uint4 x = reinterpret_cast<const uint4*>(p)[i];
                 w[4 * i] = x.x;
-                w[4 * i + 1] = x.y;
-                w[4 * i + 2] = x.z;
-                w[4 * i + 3] = x.w;
+                w[(4 * i + 1) % kWords] = x.y;
+                w[(4 * i + 2) % kWords] = x.z;
+                w[(4 * i + 3) % kWords] = x.w;
             }
+        } else if (kWords == 2) {
+            const uint2 x = *reinterpret_cast<const uint2*>(p);
+            w[0] = x.x;
+            w[1 % kWords] = x.y;
         } else {
-#pragma unroll
-            for (int i = 0; i < W; ++i) {
-                const uint2 x = *reinterpret_cast<const uint2*>(p + 8 * i);
-                w[2 * i] = x.x;
-                w[2 * i + 1] = x.y;
-            }
+            w[0] = *reinterpret_cast<const uint32_t*>(p);
         }
     }
-    // the codes of the half's coordinates 8c .. 8c + 7
+    // Exchanges piece c with piece c ^ (kSub == 4 ? 2 : 4) of the part.
+    __device__ __forceinline__ void exchange(bool yes) {
+        constexpr int kStep = SUB == 4 ? W / 2 : W;  // words from one to the other
+        if (kStep == 0) {                            // (in one word)
+            w[0] = yes ? __byte_perm(w[0], 0u, 0x1032) : w[0];
+        } else {
+#pragma unroll
+            for (int i = 0; i < kWords; ++i)
+                if (!(i & (kStep ? kStep : 1))) {
+                    const uint32_t x = w[i], y = w[(i + kStep) % kWords];
+                    w[i] = yes ? y : x;
+                    w[(i + kStep) % kWords] = yes ? x : y;
+                }
+        }
+    }
+    // the codes of the part's coordinates 8c .. 8c + 7
     __device__ __forceinline__ uint32_t codes(int c) const { return w[8 * W * c / 32] >> (8 * W * c % 32); }
 };
 
 template <int ROWS, int WK, int LK, bool PROD, int WV, int LV>
-__global__ void __launch_bounds__(kFThreads, 1)
+__global__ void __launch_bounds__(FewSmem<ROWS>::kThreads, 1)
     few_attend_kernel(const __grid_constant__ CUtensorMap q_map, const FewArgs a) {
     using M = FewSmem<ROWS>;
     extern __shared__ __align__(1024) uint8_t smem[];
@@ -163,7 +198,7 @@ __global__ void __launch_bounds__(kFThreads, 1)
     griddep_launch_dependents();
     const int slot = (int)(blockIdx.x / (unsigned)a.Hkv), hk = (int)(blockIdx.x % (unsigned)a.Hkv);
     if (blockIdx.x == 0 && blockIdx.y == 0) {
-        for (int b = threadIdx.x; b < a.B; b += kFThreads)
+        for (int b = threadIdx.x; b < a.B; b += M::kThreads)
             if (a.cu_q[b] < 0 || a.cu_q[b + 1] < a.cu_q[b] || a.cu_q[b + 1] > a.total_q)
                 atomicOr(a.err, TQ_DEVERR_SEQLEN);
     }
@@ -178,7 +213,7 @@ __global__ void __launch_bounds__(kFThreads, 1)
     if (off < 0 || kv_len > a.max_kv) {  // a length that cannot be: zero rows
         if (blockIdx.y) return;
         if (threadIdx.x == 0) atomicOr(a.err, TQ_DEVERR_SEQLEN);
-        for (int i = threadIdx.x; i < nrows * kDim; i += kFThreads) {
+        for (int i = threadIdx.x; i < nrows * kDim; i += M::kThreads) {
             const size_t o = out_row(i / kDim) * kDim + i % kDim;
             if (a.out_fp32) static_cast<float*>(a.out)[o] = 0.f;
             else static_cast<__half*>(a.out)[o] = __ushort_as_half(0);
@@ -192,15 +227,16 @@ __global__ void __launch_bounds__(kFThreads, 1)
     const int n = min(share, all - j0);
     const size_t prow0 = (size_t)blockIdx.y * a.total_q * a.Hq;
     if (n <= 0) {
-        for (int r = threadIdx.x; r < nrows; r += kFThreads) a.ml[prow0 + out_row(r)] = make_float2(-INFINITY, 0.f);
+        for (int r = threadIdx.x; r < nrows; r += M::kThreads) a.ml[prow0 + out_row(r)] = make_float2(-INFINITY, 0.f);
         return;
     }
     // roles: with 32 rows four softmax warps, on the one lane quarter that has them, share a
     // tile's tokens; with 128 one per quarter
     constexpr int kParts = ROWS == 32 ? 4 : 1;
-    const bool softmax = ROWS == 32 ? warp % 4 == 0 : warp < 4;
-    const int coder = ROWS == 32 ? (warp % 4 == 0 ? -1 : (warp / 4) * 3 + warp % 4 - 1) : warp - 4;
-    constexpr int kWarpIssue = ROWS == 32 ? 11 : 12;  // (ROWS = 32: coder 8)
+    constexpr int kSub = M::kSub, kCoders = 4 * kSub;
+    const bool softmax = ROWS == 32 ? warp % 4 == 0 && warp < 16 : warp < 4;
+    const int coder = ROWS == 32 ? (warp % 4 == 0 ? kCoders : (warp / 4) * 3 + warp % 4 - 1) : warp - 4;
+    constexpr int kWarpIssue = ROWS == 32 ? 16 : 12;
     const int live_warps = ROWS == 32 ? kParts : (nrows + 31) / 32;
 
     const uint32_t bars = sbase + M::kOffBar;
@@ -216,11 +252,11 @@ __global__ void __launch_bounds__(kFThreads, 1)
     if (threadIdx.x == 0) {
         mbar_init(bar(kFBQ), 1);
         for (int s = 0; s < 2; ++s) {
-            mbar_init(bar(kFBKFull + s), 8);
+            mbar_init(bar(kFBKFull + s), kCoders);
             mbar_init(bar(kFBKEmpty + s), (uint32_t)live_warps + 1);  // MMAs done, scalars read
         }
         for (int s = 0; s < M::kVBufs; ++s) {
-            mbar_init(bar(kFBVFull + s), 8);
+            mbar_init(bar(kFBVFull + s), kCoders);
             mbar_init(bar(kFBVEmpty + s), 1);
         }
         mbar_init(bar(kFBO), 1);
@@ -245,53 +281,60 @@ __global__ void __launch_bounds__(kFThreads, 1)
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
 
-    if (!softmax && coder < 8) {
+    if (!softmax && coder < kCoders) {
         if (ROWS != 32) set_registers_down<kFCodeRegs>();
         // ------------------------------------------------------------ codes to operands
-        const int tok = (coder & 3) * 32 + lane, half = coder >> 2, r16 = tok % kPage;
+        // the threads of a token side by side, so that a warp reads whole rows
+        const int tok = coder * (32 / kSub) + lane / kSub, sub = lane % kSub, r16 = tok % kPage;
         const uint32_t lead = lane == 0;
-        struct Raw {  // a tile's packed bytes of this thread's half token
-            HalfRow<WK> kw;
-            HalfRow<WV> vw;
-            HalfRow<1> sw;
+        struct Raw {  // a tile's packed bytes of this thread's part of its token
+            PartRow<WK, kSub> kw;
+            PartRow<WV, kSub> vw;
+            PartRow<1, kSub> sw;
             float kn, kg, vn;
-            bool bad;
+            int state;  // 0 usable, 1 behind the last token, 2 block out of range
         };
-        // block of the thread's token in tile j (nothing looks at it before fetch does)
+        // Block of the thread's token in tile j (nothing looks at it before fetch does); loads are
+        // made whether the token is there or not, from the nearest that is: a value that is loaded
+        // on one path only is copied at the paths' end, and waited for there.
         const int32_t* table = a.block_table + (size_t)b * a.max_blocks;
-        auto here = [&](int j) { return j < n && (j0 + j) * kFN + tok < kv_len; };
-        auto block_of = [&](int j) -> int {
-            int blk = 0;
-            if (here(j)) blk = table[((j0 + j) * kFN + tok) / kPage];
-            return blk;
-        };
+        auto block_of = [&](int j) -> int { return table[min((j0 + j) * kFN + tok, kv_len - 1) / kPage]; };
+        const uint8_t* kh = a.kc + (size_t)hk * a.lk.bytes;
+        const uint8_t* vh = a.vc + (size_t)hk * a.lv.bytes;
+        const size_t kstep = (size_t)a.Hkv * a.lk.bytes, vstep = (size_t)a.Hkv * a.lv.bytes;
         auto fetch = [&](Raw& r, int j, int blk) {
-            r.kn = r.kg = r.vn = 0.f;
-            r.bad = blk < 0 || blk >= a.num_blocks;
-            if (!here(j)) r.bad = false;
-            else if (!r.bad) {
-            const uint8_t* kp = a.kc + ((size_t)blk * a.Hkv + hk) * a.lk.bytes;
-            const uint8_t* vp = a.vc + ((size_t)blk * a.Hkv + hk) * a.lv.bytes;
-            r.kw.load(kp + r16 * a.lk.code_row + half * 8 * WK);
-            if (PROD) r.sw.load(kp + a.lk.signs_off + r16 * (kDim / 8) + half * 8);
-            r.vw.load(vp + r16 * a.lv.code_row + half * 8 * WV);
+            const bool in = blk >= 0 && blk < a.num_blocks;
+            r.state = j >= n || (j0 + j) * kFN + tok >= kv_len ? 1 : in ? 0 : 2;
+            const uint8_t* kp = kh + (in ? blk : 0) * kstep;
+            const uint8_t* vp = vh + (in ? blk : 0) * vstep;
+            r.kw.load(kp + r16 * a.lk.code_row + sub * (16 * WK / kSub));
+            if (PROD) r.sw.load(kp + a.lk.signs_off + r16 * (kDim / 8) + sub * (16 / kSub));
+            r.vw.load(vp + r16 * a.lv.code_row + sub * (16 * WV / kSub));
             r.kn = reinterpret_cast<const float*>(kp + a.lk.norm_off)[r16];
             if (PROD) r.kg = reinterpret_cast<const float*>(kp + a.lk.gamma_off)[r16];
             r.vn = reinterpret_cast<const float*>(vp + a.lv.norm_off)[r16];
-            }
         };
-        const uint32_t row = (uint32_t)tok * 128 + half * kFHalf;
+                // 16-byte pieces c = sub * kPer .. of the row, at c ^ (row % 8) within their half
+        constexpr int kPer = 16 / kSub;
+        const uint32_t row = (uint32_t)tok * 128 + (sub * kPer / 8) * kFHalf;
+        const int piece0 = sub * kPer % 8;
+        // eight threads that store at once (two or four tokens) hit all eight pieces of the banks:
+        // the parts of the second half go in another order
+        const int swap = kSub == 4 ? (sub >> 1) * 2 : sub * 4;
         bool ok = true;
-        auto tile = [&](const Raw& r, int j, int s) {
+        auto tile = [&](Raw& r, int j, int s) {
             if (j > 1 && !mbar_wait_all(bar(kFBKEmpty + s), (uint32_t)(j / 2 - 1) & 1u, abort, kFWaitNs)) {
                 give_up();
                 ok = false;
                 return;
             }
+            r.kw.exchange(swap != 0);
+            if (PROD) r.sw.exchange(swap != 0);
+            r.vw.exchange(swap != 0);
             uint8_t* kt = smem + M::kOffK + s * 2 * kFTile + row;
 #pragma unroll
-            for (int c = 0; c < 8; ++c) {
-                const uint32_t at = (uint32_t)(c ^ (tok & 7)) << 4;
+            for (int c = 0; c < kPer; ++c) {
+                const uint32_t at = (uint32_t)((piece0 + c) ^ swap ^ (tok & 7)) << 4;
                 uint32_t w[4];
                 levels8<WK, LK>(r.kw.codes(c), a.tk, w);
                 *reinterpret_cast<uint4*>(kt + at) = make_uint4(w[0], w[1], w[2], w[3]);
@@ -300,22 +343,22 @@ __global__ void __launch_bounds__(kFThreads, 1)
                     *reinterpret_cast<uint4*>(kt + kFTile + at) = make_uint4(w[0], w[1], w[2], w[3]);
                 }
             }
-            if (half == 0) {
+            if (sub == 0) {
                 float* scal = reinterpret_cast<float*>(smem + M::kOffScal) + s * 256 + tok;
-                scal[0] = r.kn * a.qscale;
-                if (PROD) scal[128] = r.kg * a.sscale;
+                scal[0] = r.state ? 0.f : r.kn * a.qscale;
+                if (PROD) scal[128] = r.state ? 0.f : r.kg * a.sscale;
                 if (r16 == 0) {
-                    page_bad[8 * s + tok / kPage] = r.bad;
-                    if (r.bad) atomicOr(a.err, TQ_DEVERR_BLOCK);
+                    page_bad[8 * s + tok / kPage] = r.state == 2;
+                    if (r.state == 2) atomicOr(a.err, TQ_DEVERR_BLOCK);
                 }
             }
             fence_proxy_async_shared();
             mbar_arrive_lead(lead, bar(kFBKFull + s));
             // the values of a token that is not finite are left out here and make the rows that
             // attend it NaN at the end: a masked one must not reach any
-            const float vn = r.vn * a.vscale;
+            const float vn = r.state ? 0.f : r.vn * a.vscale;
             const bool fine = isfinite(vn);
-            if (!fine && half == 0) atomicMin(first_bad, (j0 + j) * kFN + tok);
+            if (!fine && sub == 0) atomicMin(first_bad, (j0 + j) * kFN + tok);
             const __half2 v2 = __float2half2_rn(fine ? vn : 0.f);
             const int vb = j % M::kVBufs, use = j / M::kVBufs;
             if (use > 0 && !mbar_wait_all(bar(kFBVEmpty + vb), (uint32_t)(use - 1) & 1u, abort, kFWaitNs)) {
@@ -325,7 +368,7 @@ __global__ void __launch_bounds__(kFThreads, 1)
             }
             uint8_t* vt = smem + M::kOffV + vb * kFTile + row;
 #pragma unroll
-            for (int c = 0; c < 8; ++c) {
+            for (int c = 0; c < kPer; ++c) {
                 uint32_t w[4];
                 levels8<WV, LV>(r.vw.codes(c), a.tv, w);
 #pragma unroll
@@ -333,7 +376,7 @@ __global__ void __launch_bounds__(kFThreads, 1)
                     const __half2 x = __hmul2(*reinterpret_cast<const __half2*>(&w[i]), v2);
                     w[i] = *reinterpret_cast<const uint32_t*>(&x);
                 }
-                *reinterpret_cast<uint4*>(vt + ((uint32_t)(c ^ (tok & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+                *reinterpret_cast<uint4*>(vt + ((uint32_t)((piece0 + c) ^ swap ^ (tok & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
             }
             fence_proxy_async_shared();
             mbar_arrive_lead(lead, bar(kFBVFull + vb));
@@ -422,6 +465,7 @@ __global__ void __launch_bounds__(kFThreads, 1)
         if (ROWS == 32 || warp < live_warps) {
         // ------------------------------------------------------------ softmax
         constexpr int kCols = kFN / kParts, kChunks = kCols / 32;  // tokens of this thread
+        constexpr bool kPolyPairs = ROWS == 32;  // every other pair: one sub-partition's pipe serves all four warps
         const int part = ROWS == 32 ? warp / 4 : 0, row = ROWS == 32 ? lane : (int)threadIdx.x;
         const uint32_t lanes = ROWS == 32 ? 0u : (uint32_t)warp << 21, lead = lane == 0;
         const uint32_t ts = tmem + lanes + kCols * part, tp = tmem + kFColP + kCols / 2 * part + lanes;
@@ -446,19 +490,20 @@ __global__ void __launch_bounds__(kFThreads, 1)
             uint32_t s[kChunks][32];
             const float4* sc = reinterpret_cast<const float4*>(smem + M::kOffScal + (j & 1) * 1024) + kCols / 4 * part;
 #pragma unroll
-            for (int q = 0; q < kChunks; ++q) {
-                uint32_t d2[32];
-                tmem_ld32(ts + 32 * q, s[q]);
-                if (PROD) tmem_ld32(ts + kFColS2 + 32 * q, d2);
+            for (int q = 0; q < 2 * kChunks; ++q) {  // 16 tokens
+                uint32_t d1[16], d2[16];
+                tmem_ld16(ts + 16 * q, d1);
+                if (PROD) tmem_ld16(ts + kFColS2 + 16 * q, d2);
                 tmem_ld_wait();
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {  // four tokens
-                    const float4 fa = sc[8 * q + e];
-                    uint32_t* x = &s[q][4 * e];
-                    float2 u = __fmul2_rn(make_float2(fa.x, fa.y), make_float2(__uint_as_float(x[0]), __uint_as_float(x[1])));
-                    float2 v = __fmul2_rn(make_float2(fa.z, fa.w), make_float2(__uint_as_float(x[2]), __uint_as_float(x[3])));
+                for (int e = 0; e < 4; ++e) {  // four tokens
+                    const float4 fa = sc[4 * q + e];
+                    uint32_t* x = &s[q / 2][16 * (q & 1) + 4 * e];
+                    const uint32_t* z = &d1[4 * e];
+                    float2 u = __fmul2_rn(make_float2(fa.x, fa.y), make_float2(__uint_as_float(z[0]), __uint_as_float(z[1])));
+                    float2 v = __fmul2_rn(make_float2(fa.z, fa.w), make_float2(__uint_as_float(z[2]), __uint_as_float(z[3])));
                     if (PROD) {
-                        const float4 fb = sc[32 + 8 * q + e];
+                        const float4 fb = sc[32 + 4 * q + e];
                         const uint32_t* y = &d2[4 * e];
                         u = __ffma2_rn(make_float2(fb.x, fb.y), make_float2(__uint_as_float(y[0]), __uint_as_float(y[1])), u);
                         v = __ffma2_rn(make_float2(fb.z, fb.w), make_float2(__uint_as_float(y[2]), __uint_as_float(y[3])), v);
@@ -551,8 +596,12 @@ __global__ void __launch_bounds__(kFThreads, 1)
                     const int i = 16 * q + 2 * e;
                     float2 x = make_float2(__uint_as_float(s[i / 32][i % 32]), __uint_as_float(s[i / 32][i % 32 + 1]));
                     x = __fadd2_rn(x, nm);
-                    x.x = few_ex2(x.x);
-                    x.y = few_ex2(x.y);
+                    if (kPolyPairs && (e & 1)) {
+                        x = few_ex2_poly(x);  // (a NaN row has its other pairs' NaN)
+                    } else {
+                        x.x = few_ex2(x.x);
+                        x.y = few_ex2(x.y);
+                    }
                     sum[e & 1] = __fadd2_rn(sum[e & 1], x);
                     const __half2 hp = __floats2half2_rn(x.x, x.y);
                     p[q][e] = *reinterpret_cast<const uint32_t*>(&hp);
@@ -795,7 +844,7 @@ cudaError_t launch_few_attend(const CUtensorMap& q, const FewArgs& a, dim3 grid,
     static std::atomic<uint64_t> ready{0};
     const cudaError_t e = ready_kernel(k, ready, (int)FewSmem<ROWS>::kBytes, ROWS == 32 ? 0 : kFRegs);  // (the split has to add up)
     if (e != cudaSuccess) return e;
-    return launch_after(k, grid, kFThreads, FewSmem<ROWS>::kBytes, stream, q, a);
+    return launch_after(k, grid, FewSmem<ROWS>::kThreads, FewSmem<ROWS>::kBytes, stream, q, a);
 }
 
 }  // namespace

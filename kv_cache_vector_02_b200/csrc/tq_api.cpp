@@ -565,6 +565,7 @@ tq_status tq_chunk_attention(const tq_ctx* ctx, const uint16_t* q, const int32_t
     if (Hq % Hkv != 0 || Hq / Hkv > 128) return TQ_ERR_INVALID_ARG;
     if (!(scale >= 0.f) || !std::isfinite(scale)) return TQ_ERR_INVALID_ARG;
     if (B == 0 || total_q == 0) return TQ_OK;
+    if (num_blocks < 1) return TQ_ERR_INVALID_ARG;
     if (!q || !cu_q || !k_cache || !v_cache || !block_table || !seq_lens || !out || !workspace)
         return TQ_ERR_INVALID_ARG;
     if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(out) || !aligned16(workspace))
