@@ -320,6 +320,7 @@ TQ_API tq_status tq_rope_plan(int rot_dim, int layout, double base, int scaling,
  * in fp32, rounded once; coordinates from rot_dim on are copied.  transpose != 0 applies
  * the transposed map (-a instead of a): the gradient with respect to the inputs given the
  * gradient of the outputs, and for mscale = 1 the inverse.
+ *   Hq, Hkv      : 1 .. 2048.
  *   q_dev, k_dev : fp16 rows of Hq (Hkv) heads of 128, q_stride (k_stride) elements from one
  *                  token to the next (a multiple of 8, >= heads * 128): views into a fused
  *                  projection work as they are.  Either may be NULL (its heads are then not

@@ -473,7 +473,7 @@ tq_status tq_rope(const tq_rope_table* table, const uint16_t* q, int64_t q_strid
     if (!q && !k) return TQ_ERR_INVALID_ARG;
     if (!q) Hq = 0;
     if (!k) Hkv = 0;
-    if ((q && Hq < 1) || (k && Hkv < 1) || Hq > 65536 || Hkv > 65536) return TQ_ERR_INVALID_ARG;
+    if ((q && Hq < 1) || (k && Hkv < 1) || Hq > 2048 || Hkv > 2048) return TQ_ERR_INVALID_ARG;
     if (!positions || (q && !q_out) || (k && !k_out)) return TQ_ERR_INVALID_ARG;
     if ((q && (!good_stride(q_stride, Hq) || !good_stride(q_out_stride, Hq))) ||
         (k && (!good_stride(k_stride, Hkv) || !good_stride(k_out_stride, Hkv))))
