@@ -394,8 +394,11 @@ TQ_API size_t tq_chunk_workspace_bytes(const tq_ctx* ctx, int B, int total_q, in
  *   out_dev        : [total_q][Hq][128], fp16 (out_fp32 = 0) or fp32 (out_fp32 = 1); rows in
  *                    no sequence are left as they were.  Must not overlap q or the workspace.
  *   workspace_dev  : >= tq_chunk_workspace_bytes(...) bytes, 16-byte aligned.
- * A cache row behind a sequence's last token may hold anything.  The launches are queued on
- * stream, on the context's device; total_q = 0 or B = 0 launches nothing.
+ * A cache row behind a sequence's last token may hold anything, and a token's norms that are
+ * not finite reach the queries that attend it only (for value norms up to 2^14 sqrt(d), beyond
+ * which its values overflow fp16).  Three launches, or with many queries two or three for as
+ * many kv heads as fit 1 GiB of decompressed tokens at a time, queued on stream, on the
+ * context's device; total_q = 0 or B = 0 launches nothing.
  */
 TQ_API tq_status tq_chunk_attention(const tq_ctx* ctx, const uint16_t* q_dev, const int32_t* cu_q_dev,
                                     const uint8_t* k_cache_dev, const uint8_t* v_cache_dev, int num_blocks,

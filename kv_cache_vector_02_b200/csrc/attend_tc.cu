@@ -19,12 +19,25 @@
 // 512), but scores are there only until their softmax has them in registers: the halves
 // share one score buffer in turn, and P has columns of its own.  So the next scores are
 // computed while the softmax before them runs, and no softmax waits for the tensor core.
+// The warps that are not softmax move their registers to it (200 a thread: 128 scores).
+//
+// Bound (8192 tokens, 64 query heads over 8: 1.1 ms, 990 TFLOP/s, 59 % of the measured GEMM): a
+// pair of 128 x 128 tiles takes 3180 cycles where its MMAs alone take 2080 and its
+// exponentials, 16 a cycle and SM, 2050.  What is between is the chain from a softmax over
+// the barriers to the MMAs and back (a satisfied wait costs about 100 cycles, an arrive 200)
+// and the power limit: the SMs run at about 1.45 GHz.  On the way: scores written over by P,
+// one tile in flight per half, 4800 cycles; MMAs issued by a converged warp, and two buffers
+// of 64 tokens, 3830 (an MMA of N = 64 takes as long as one of 128); one shared buffer of 128,
+// 3180.  Tried on that: two threads per row (3390), an issuer warp each for S and P V (3340 to
+// 3700), a branch per stage with constant descriptors (4150), an eighth to a half of the
+// exponentials by a polynomial (3390 to 3490), tests of the barriers without a pause (3720).
+//
 // O is rescaled only when a row's maximum has grown by more than 2^8 since the one it is
 // scaled by: P stays below 2^8, far inside fp16, and the sum is exact about it either way.
 //
 // Masked places may hold anything.  Scores are masked by position, whatever their value.
 // P there is 0, but 0 * inf or 0 * NaN in V would reach O: tiles with a masked (row,
-// token) pair are first looked through by warps 10 and 11, which clear non-finite values
+// token) pair are first looked through by warps 10, 11, which clear non-finite values
 // in shared memory and note it; a row's epilogue then adds those values back (v * p is v
 // for p > 0 and v infinite or NaN) for the tokens the row does attend.
 #include <cuda.h>
@@ -219,170 +232,173 @@ __global__ void __launch_bounds__(kAThreads, 1)
 
     if (warp >= 8) {
         set_registers_down<kAOtherRegs>();
-    if (warp == 9) {
-        // ------------------------------------------------------------ producer
-        if (lane == 0) {
-            int kj = 0, vj = 0;
-            const int half_bytes = a.G * a.QT * 128;
-            mbar_arrive_expect_tx(bar(kABQ), (uint32_t)(half_bytes * 4));
-            for (int h = 0; h < 2; ++h)
-                for (int x = 0; x < 2; ++x)
-                    tma_load_3d(sbase + kAOffQ + h * kATile + x * kAHalf, &tq_map, 64 * x, (a.head0 + hk) * a.G,
-                                c0 + q0 + h * a.QT, bar(kABQ));
-            auto load = [&](const void* map, int full, int empty, uint32_t at, int stages, int j) -> bool {
-                const int s = j % stages;
-                if (!mbar_wait(bar(empty + s), (uint32_t)(j / stages & 1) ^ 1u, abort, kAWaitNs)) {
-                    give_up();
-                    return false;
-                }
-                mbar_arrive_expect_tx(bar(full + s), kATile);
-                for (int x = 0; x < 2; ++x)
-                    tma_load_3d(sbase + at + s * kATile + x * kAHalf, map, 64 * x, hk, kv_row + j * kAN, bar(full + s));
-                return true;
-            };
-            bool ok = load(&tk_map, kABKFull, kABKEmpty, kAOffK, kAKStages, 0);
-            kj = ok;
-            for (int j = 0; ok && j < n; ++j) {
-                if (j + 1 < n) {
-                    ok = load(&tk_map, kABKFull, kABKEmpty, kAOffK, kAKStages, j + 1);
-                    kj += ok;
-                }
-                if (ok) {
-                    ok = load(&tv_map, kABVFull, kABVEmpty, kAOffV, kAVStages, j);
-                    vj += ok;
-                    if (ok && j >= masked_from) mbar_arrive(bar(kABVGo + j % kAVStages));
-                }
-            }
-            // every copy lands before the CTA can exit
-            const volatile int never = 0;
-            mbar_wait(bar(kABQ), 0, &never, kAWaitNs);
-            for (int j = max(0, kj - kAKStages); j < kj; ++j)
-                mbar_wait(bar(kABKFull + j % kAKStages), (uint32_t)(j / kAKStages) & 1u, &never, kAWaitNs);
-            for (int j = max(0, vj - kAVStages); j < vj; ++j)
-                mbar_wait(bar(kABVFull + j % kAVStages), (uint32_t)(j / kAVStages) & 1u, &never, kAWaitNs);
-        }
-        __syncwarp();
-    } else if (warp == 8) {
-        // ------------------------------------------------------------ MMA issuer
-        // (the whole warp, converged: see umma_ss_warp; all 512 columns are ours, from 0 on)
-        constexpr uint32_t id_s = idesc_f16(128, kAN), id_o = idesc_f16(128, kDim) | (1u << 16);
-        const uint32_t q_lo = sw128_desc_lo(sbase + kAOffQ), k_lo = sw128_desc_lo(sbase + kAOffK);
-        const uint32_t v_lo = v_desc_lo(sbase + kAOffV);
-        auto wait = [&](int i, uint32_t parity) -> bool {
-            if (mbar_wait_all(bar(i), parity & 1u, abort, kAWaitNs)) return true;
-            if (lane == 0) give_up();
-            return false;
-        };
-        const uint32_t lead = elect_lane();
-        auto scores = [&](int h, int stage) {
-            const uint32_t ql = q_lo + h * (kATile >> 4), kl = k_lo + stage * (kATile >> 4);
-#pragma unroll
-            for (int ks = 0; ks < 8; ++ks) {
-                const uint32_t o = (uint32_t)(ks & 3) * 2 + (uint32_t)(ks >> 2) * (kAHalf >> 4);
-                umma_ss_warp(lead, 0, sw128_desc(ql + o), sw128_desc(kl + o), id_s, ks > 0);
-            }
-            umma_commit_warp(lead, bar(kABS + h));
-        };
-        auto values = [&](int h, int stage, bool first) {
-            const uint32_t vl = v_lo + stage * (kATile >> 4);
-#pragma unroll
-            for (int ks = 0; ks < 8; ++ks)
-                umma_ts_warp(lead, kColO + h * 128, kColP + h * 64 + ks * 8, sw128_desc(vl + ks * (2048 >> 4)), id_o,
-                             !(first && ks == 0));
-            umma_commit_warp(lead, bar(kABO + h));
-        };
-        bool ok = tmem == 0;
-        if (!ok && lane == 0) {
-            *abort = 1;
-            atomicOr(a.err, TQ_DEVERR_INTERNAL);
-        }
-        ok = ok && wait(kABQ, 0) && wait(kABKFull, 0);
-        int user = -1;               // whose scores the buffer last held, and of which tile
-        uint32_t used = 0;
-        auto next_scores = [&](int h, int j, int stage) {
-            if (ok && user >= 0) ok = wait(kABL + user, used);
-            if (!ok) return;
-            tc_fence_after();
-            scores(h, stage);
-            user = h;
-            used = (uint32_t)j;
-        };
-        if (n0) next_scores(0, 0, 0);
-        if (n1) next_scores(1, 0, 0);
-        if (ok) umma_commit_warp(lead, bar(kABKEmpty));
-        int vs = 0, kn = 0;          // stages of tile j's values and of tile j + 1's keys
-        uint32_t vp = 0, kp = 0;     // and their phases
-        for (int j = 0; ok && j < n; ++j) {
-            if (++kn == kAKStages) {
-                kn = 0;
-                kp ^= 1u;
-            }
-            if (j + 1 < n) ok = wait(kABKFull + kn, kp);
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int nh = h ? n1 : n0;
-                if (j + 1 < nh) next_scores(h, j + 1, kn);
-                if (ok && h == 0)
-                    ok = j >= masked_from ? wait(kABVClean + vs, (j - masked_from) / kAVStages) : wait(kABVFull + vs, vp);
-                if (ok && j < nh) {
-                    ok = wait(kABP + h, j);
+        if (warp == 9) {
+            // ------------------------------------------------------------ producer
+            if (lane == 0) {
+                int kj = 0, vj = 0;
+                const int half_bytes = a.G * a.QT * 128;
+                mbar_arrive_expect_tx(bar(kABQ), (uint32_t)(half_bytes * 4));
+                for (int h = 0; h < 2; ++h)
+                    for (int x = 0; x < 2; ++x)
+                        tma_load_3d(sbase + kAOffQ + h * kATile + x * kAHalf, &tq_map, 64 * x, (a.head0 + hk) * a.G,
+                                    c0 + q0 + h * a.QT, bar(kABQ));
+                auto load = [&](const void* map, int full, int empty, uint32_t at, int stages, int j) -> bool {
+                    const int s = j % stages;
+                    if (!mbar_wait(bar(empty + s), (uint32_t)(j / stages & 1) ^ 1u, abort, kAWaitNs)) {
+                        give_up();
+                        return false;
+                    }
+                    mbar_arrive_expect_tx(bar(full + s), kATile);
+                    for (int x = 0; x < 2; ++x)
+                        tma_load_3d(sbase + at + s * kATile + x * kAHalf, map, 64 * x, hk, kv_row + j * kAN,
+                                    bar(full + s));
+                    return true;
+                };
+                bool ok = load(&tk_map, kABKFull, kABKEmpty, kAOffK, kAKStages, 0);
+                kj = ok;
+                for (int j = 0; ok && j < n; ++j) {
+                    if (j + 1 < n) {
+                        ok = load(&tk_map, kABKFull, kABKEmpty, kAOffK, kAKStages, j + 1);
+                        kj += ok;
+                    }
                     if (ok) {
-                        tc_fence_after();
-                        values(h, vs, j == 0);
+                        ok = load(&tv_map, kABVFull, kABVEmpty, kAOffV, kAVStages, j);
+                        vj += ok;
+                        if (ok && j >= masked_from) mbar_arrive(bar(kABVGo + j % kAVStages));
                     }
                 }
+                // every copy lands before the CTA can exit
+                const volatile int never = 0;
+                mbar_wait(bar(kABQ), 0, &never, kAWaitNs);
+                for (int j = max(0, kj - kAKStages); j < kj; ++j)
+                    mbar_wait(bar(kABKFull + j % kAKStages), (uint32_t)(j / kAKStages) & 1u, &never, kAWaitNs);
+                for (int j = max(0, vj - kAVStages); j < vj; ++j)
+                    mbar_wait(bar(kABVFull + j % kAVStages), (uint32_t)(j / kAVStages) & 1u, &never, kAWaitNs);
             }
-            if (!ok) break;
-            umma_commit_warp(lead, bar(kABVEmpty + vs));
-            if (j + 1 < n) umma_commit_warp(lead, bar(kABKEmpty + kn));
-            if (++vs == kAVStages) {
-                vs = 0;
-                vp ^= 1u;
-            }
-        }
-        // nothing is in flight when the CTA exits
-        umma_commit_warp(lead, bar(kABDrain));
-        const volatile int never = 0;
-        mbar_wait(bar(kABDrain), 0, &never, kAWaitNs);
-        __syncwarp();
-    } else {
-        // ------------------------------------------------------------ masked tiles' values
-        for (int j = masked_from; j < n; ++j) {
-            const int s = j % kAVStages;
-            // (these warps do not follow the unmasked tiles' phases of the stage: its load's
-            // issue tells them that the phase of this tile is the current one)
-            if (!__all_sync(0xffffffffu, mbar_wait_asleep(bar(kABVGo + s), (uint32_t)((j - masked_from) / kAVStages) & 1u, abort, kAWaitNs)) ||
-                !mbar_wait_warp(bar(kABVFull + s), (uint32_t)(j / kAVStages) & 1u, abort, kAWaitNs)) {
-                give_up();
-                break;
-            }
-            uint4* v = reinterpret_cast<uint4*>(smem + kAOffV + s * kATile);
-            bool any = false;
-#pragma unroll 4
-            for (int i = threadIdx.x - 320; i < (int)(kATile / 16); i += 64) {
-                uint4 x = v[i];
-                uint32_t w[4] = {x.x, x.y, x.z, x.w};
-                bool bad = false;
+            __syncwarp();
+        } else if (warp == 8) {
+            // ------------------------------------------------------------ MMA issuer
+            // (the whole warp, converged: see umma_ss_warp; all 512 columns are ours, from 0 on)
+            constexpr uint32_t id_s = idesc_f16(128, kAN), id_o = idesc_f16(128, kDim) | (1u << 16);
+            const uint32_t q_lo = sw128_desc_lo(sbase + kAOffQ), k_lo = sw128_desc_lo(sbase + kAOffK);
+            const uint32_t v_lo = v_desc_lo(sbase + kAOffV);
+            auto wait = [&](int i, uint32_t parity) -> bool {
+                if (mbar_wait_all(bar(i), parity & 1u, abort, kAWaitNs)) return true;
+                if (lane == 0) give_up();
+                return false;
+            };
+            const uint32_t lead = elect_lane();
+            auto scores = [&](int h, int stage) {
+                const uint32_t ql = q_lo + h * (kATile >> 4), kl = k_lo + stage * (kATile >> 4);
 #pragma unroll
-                for (int p = 0; p < 4; ++p) {
-                    // bit 15 / 31: the half's exponent is all ones
-                    const uint32_t e = ((w[p] & 0x7C007C00u) + 0x04000400u) & 0x80008000u;
-                    if (e) {
-                        bad = true;
-                        if (e & 0x8000u) w[p] &= 0xFFFF0000u;
-                        if (e & 0x80000000u) w[p] &= 0x0000FFFFu;
+                for (int ks = 0; ks < 8; ++ks) {
+                    const uint32_t o = (uint32_t)(ks & 3) * 2 + (uint32_t)(ks >> 2) * (kAHalf >> 4);
+                    umma_ss_warp(lead, 0, sw128_desc(ql + o), sw128_desc(kl + o), id_s, ks > 0);
+                }
+                umma_commit_warp(lead, bar(kABS + h));
+            };
+            auto values = [&](int h, int stage, bool first) {
+                const uint32_t vl = v_lo + stage * (kATile >> 4);
+#pragma unroll
+                for (int ks = 0; ks < 8; ++ks)
+                    umma_ts_warp(lead, kColO + h * 128, kColP + h * 64 + ks * 8, sw128_desc(vl + ks * (2048 >> 4)),
+                                 id_o, !(first && ks == 0));
+                umma_commit_warp(lead, bar(kABO + h));
+            };
+            bool ok = tmem == 0;
+            if (!ok && lane == 0) {
+                *abort = 1;
+                atomicOr(a.err, TQ_DEVERR_INTERNAL);
+            }
+            ok = ok && wait(kABQ, 0) && wait(kABKFull, 0);
+            int user = -1;               // whose scores the buffer last held, and of which tile
+            uint32_t used = 0;
+            auto next_scores = [&](int h, int j, int stage) {
+                if (ok && user >= 0) ok = wait(kABL + user, used);
+                if (!ok) return;
+                tc_fence_after();
+                scores(h, stage);
+                user = h;
+                used = (uint32_t)j;
+            };
+            if (n0) next_scores(0, 0, 0);
+            if (n1) next_scores(1, 0, 0);
+            if (ok) umma_commit_warp(lead, bar(kABKEmpty));
+            int vs = 0, kn = 0;          // stages of tile j's values and of tile j + 1's keys
+            uint32_t vp = 0, kp = 0;     // and their phases
+            for (int j = 0; ok && j < n; ++j) {
+                if (++kn == kAKStages) {
+                    kn = 0;
+                    kp ^= 1u;
+                }
+                if (j + 1 < n) ok = wait(kABKFull + kn, kp);
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int nh = h ? n1 : n0;
+                    if (j + 1 < nh) next_scores(h, j + 1, kn);
+                    if (ok && h == 0)
+                        ok = j >= masked_from ? wait(kABVClean + vs, (j - masked_from) / kAVStages)
+                                              : wait(kABVFull + vs, vp);
+                    if (ok && j < nh) {
+                        ok = wait(kABP + h, j);
+                        if (ok) {
+                            tc_fence_after();
+                            values(h, vs, j == 0);
+                        }
                     }
                 }
-                if (bad) {
-                    any = true;
-                    v[i] = make_uint4(w[0], w[1], w[2], w[3]);
+                if (!ok) break;
+                umma_commit_warp(lead, bar(kABVEmpty + vs));
+                if (j + 1 < n) umma_commit_warp(lead, bar(kABKEmpty + kn));
+                if (++vs == kAVStages) {
+                    vs = 0;
+                    vp ^= 1u;
                 }
             }
-            if (any) *repaired = 1;
-            fence_proxy_async_shared();
-            mbar_arrive_warp(bar(kABVClean + s));
+            // nothing is in flight when the CTA exits
+            umma_commit_warp(lead, bar(kABDrain));
+            const volatile int never = 0;
+            mbar_wait(bar(kABDrain), 0, &never, kAWaitNs);
+            __syncwarp();
+        } else {
+            // ------------------------------------------------------------ masked tiles' values
+            for (int j = masked_from; j < n; ++j) {
+                const int s = j % kAVStages;
+                // (these warps do not follow the unmasked tiles' phases of the stage: its load's
+                // issue tells them that the phase of this tile is the current one)
+                const uint32_t go = (uint32_t)((j - masked_from) / kAVStages) & 1u;
+                if (!__all_sync(0xffffffffu, mbar_wait_asleep(bar(kABVGo + s), go, abort, kAWaitNs)) ||
+                    !mbar_wait_warp(bar(kABVFull + s), (uint32_t)(j / kAVStages) & 1u, abort, kAWaitNs)) {
+                    give_up();
+                    break;
+                }
+                uint4* v = reinterpret_cast<uint4*>(smem + kAOffV + s * kATile);
+                bool any = false;
+#pragma unroll 4
+                for (int i = threadIdx.x - 320; i < (int)(kATile / 16); i += 64) {
+                    uint4 x = v[i];
+                    uint32_t w[4] = {x.x, x.y, x.z, x.w};
+                    bool bad = false;
+#pragma unroll
+                    for (int p = 0; p < 4; ++p) {
+                        // bit 15 / 31: the half's exponent is all ones
+                        const uint32_t e = ((w[p] & 0x7C007C00u) + 0x04000400u) & 0x80008000u;
+                        if (e) {
+                            bad = true;
+                            if (e & 0x8000u) w[p] &= 0xFFFF0000u;
+                            if (e & 0x80000000u) w[p] &= 0x0000FFFFu;
+                        }
+                    }
+                    if (bad) {
+                        any = true;
+                        v[i] = make_uint4(w[0], w[1], w[2], w[3]);
+                    }
+                }
+                if (any) *repaired = 1;
+                fence_proxy_async_shared();
+                mbar_arrive_warp(bar(kABVClean + s));
+            }
         }
-    }
     } else {
         set_registers_up<kASoftmaxRegs>();
         // ------------------------------------------------------------ softmax
@@ -435,7 +451,8 @@ __global__ void __launch_bounds__(kAThreads, 1)
             for (int q = 0; q < 4; ++q) {
                 mx[q] = max3(__uint_as_float(s[q][0]), __uint_as_float(s[q][1]), __uint_as_float(s[q][2]));
 #pragma unroll
-                for (int e = 3; e < 31; e += 2) mx[q] = max3(mx[q], __uint_as_float(s[q][e]), __uint_as_float(s[q][e + 1]));
+                for (int e = 3; e < 31; e += 2)
+                    mx[q] = max3(mx[q], __uint_as_float(s[q][e]), __uint_as_float(s[q][e + 1]));
                 mx[q] = max3(mx[q], mx[q], __uint_as_float(s[q][31]));
             }
             float top = max3(max3(mx[0], mx[1], mx[2]), mx[3], mx[3]) * a.scale_log2;
@@ -511,7 +528,8 @@ __global__ void __launch_bounds__(kAThreads, 1)
                 for (int i = 0; i < 32; ++i) f[i] = __uint_as_float(o[i]) * inv;
                 if (fix) {
                     for (int t = masked_from * kAN; t <= limit; ++t) {
-                        const __half* v = reinterpret_cast<const __half*>(a.v) + (kv_row + t) * a.v_stride + hk * kDim + 32 * q;
+                        const __half* v =
+                            reinterpret_cast<const __half*>(a.v) + (kv_row + t) * a.v_stride + hk * kDim + 32 * q;
 #pragma unroll
                         for (int i = 0; i < 32; ++i) {
                             const float x = __half2float(v[i]);
@@ -584,7 +602,8 @@ cudaError_t launch_attend(const tq_ctx* ctx, const AttendCall& c, cudaStream_t s
     // slots of all sequences: floor(total / q) + B bounds every sequence's last one
     const long long slots = (long long)c.total_q / (2 * a.QT) + c.B;
     if (slots * c.heads > 0x7FFFFFFFll) return cudaErrorInvalidValue;
-    attend_tc_kernel<<<dim3((unsigned)(slots * c.heads), (unsigned)(c.splits > 1 ? c.splits : 1)), kAThreads, kASmem, stream>>>(mq, mk, mv, a);
+    const dim3 grid((unsigned)(slots * c.heads), (unsigned)(c.splits > 1 ? c.splits : 1));
+    attend_tc_kernel<<<grid, kAThreads, kASmem, stream>>>(mq, mk, mv, a);
     e = cudaGetLastError();
     if (e == cudaSuccess) count_launches(1);
     return e;

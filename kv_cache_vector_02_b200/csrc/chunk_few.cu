@@ -7,20 +7,28 @@
 //   acc = sum_t p_t (n_t / sqrt(d)) c_v,   o = R acc / sum_t p_t.
 //
 // few_rotate_kernel   q' and s of every (query, head), fp16 (R^T as fp16 hi + lo)
-// few_attend_kernel   one CTA per (128 rows, kv head, split of the tokens); a row is a
+// few_attend_kernel   one CTA per (32 or 128 rows, kv head, split of the tokens); a row is a
 //                     (query, query head of the group) pair.  Per tile of 128 tokens:
-//   8 warps     two threads per token (32 rows at most: 16 warps, four): its packed codes and signs (loaded a tile ahead)
-//               become fp16 levels and +-1 in registers, the values' times n_t/sqrt(d)
-//               (rounded to fp16, as decompressed values are), and go to swizzled
-//               operand tiles; a_t, b_t to shared memory
-//   1 warp      D1 = Q' C_k^T, D2 = S_q Sigma^T, O += P V on tcgen05
-//   4 warps     one thread per row (32 rows at most: four per row): s = a_t D1 + b_t D2 (fp32; the score's two scalars are
-//               never rounded), mask, running maximum and sum, P to tensor memory.  Warps
-//               without a row only keep step.
+//   coding warps   two threads per token (32 rows: 16 warps, four per token) turn its packed
+//                  codes and signs, loaded two tiles ahead, into fp16 levels and +-1 in
+//                  registers, the values' times n_t/sqrt(d) (rounded to fp16, as decompressed
+//                  values are), and store them to swizzled operand tiles; a_t, b_t go to shared
+//                  memory
+//   issuing warp   D1 = Q' C_k^T, D2 = S_q Sigma^T, O += P V on tcgen05
+//   softmax warps  one thread per row: s = a_t D1 + b_t D2 in fp32 (the score's two scalars are
+//                  never rounded), mask, running maximum and sum, P to tensor memory; with 32
+//                  rows four warps share a tile's tokens, 32 each
 // few_join_kernel     the splits joined, o = R acc / l in fp32
 //
-// A tile takes 24 MMAs of 65 cycles (16 without signs) whatever the rows, which is what bounds
-// it: 1560 cycles for 20 KB of pages.
+// Bound (32 sequences, 1 to 8 queries of 32 heads, about 3600 tokens each: 145 us, 1.0 TB/s of
+// pages; 137 of it in the attend kernel): the decoding.  A tile is about 8000 warp instructions
+// of lookups, two thirds of them on the ALU pipe at half rate, on the three sub-partitions that
+// the softmax leaves; a capture has the ALU pipe at 45 % over the whole kernel, the tensor pipe
+// at 31 %, DRAM at 13 %.  The MMAs of a tile, 24 of 65 cycles whatever the rows, would allow
+// 1560 cycles where it takes about 4000.  On the way: decompressing to fp16 first, 305 us; one
+// register set and one value buffer, 255; two of each up to 32 rows, 171; four softmax warps, 145.
+// Tried: four copies of the rows, one per lane quarter, each with its own softmax warp and a
+// single value buffer, 205; half of the exponentials by a polynomial, 149 against 148.
 #include <cmath>
 
 #include <cuda.h>
@@ -108,25 +116,6 @@ __device__ __forceinline__ float few_max3(float x, float y, float z) {
     float m;
     asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(m) : "f"(x), "f"(y), "f"(z));
     return m;
-}
-
-// 2^x of a pair on the FMA pipe: n = round(x) by adding 1.5 * 2^23 (its low bits are n), f = x - n
-// in [-1/2, 1/2], 2^f by the polynomial of degree 4 with the smallest relative error there
-// (Remez exchange: 2.7e-6, far below P's rounding to fp16), and n added to the exponent.
-// Below -126 the result is 2^-126, which is 0 in fp16.  A NaN gives some number.
-__device__ __forceinline__ float2 few_ex2_poly(float2 x) {
-    const float2 magic = make_float2(12582912.f, 12582912.f), minus = make_float2(-12582912.f, -12582912.f);
-    x.x = fmaxf(x.x, -126.f);
-    x.y = fmaxf(x.y, -126.f);
-    const float2 t = __fadd2_rn(x, magic), r = __fadd2_rn(t, minus);
-    const float2 f = __ffma2_rn(r, make_float2(-1.f, -1.f), x);
-    float2 p = __ffma2_rn(f, make_float2(0.009570102207362652f, 0.009570102207362652f),
-                          make_float2(0.05591785907745361f, 0.05591785907745361f));
-    p = __ffma2_rn(p, f, make_float2(0.240247443318367f, 0.240247443318367f));
-    p = __ffma2_rn(p, f, make_float2(0.6931217908859253f, 0.6931217908859253f));
-    p = __ffma2_rn(p, f, make_float2(0.9999992847442627f, 0.9999992847442627f));
-    return make_float2(__int_as_float(__float_as_int(p.x) + (__float_as_int(t.x) << 23)),
-                       __int_as_float(__float_as_int(p.y) + (__float_as_int(t.y) << 23)));
 }
 
 // Named barriers of n threads: whether x holds in any of them; plain.
@@ -465,7 +454,6 @@ __global__ void __launch_bounds__(FewSmem<ROWS>::kThreads, 1)
         if (ROWS == 32 || warp < live_warps) {
         // ------------------------------------------------------------ softmax
         constexpr int kCols = kFN / kParts, kChunks = kCols / 32;  // tokens of this thread
-        constexpr bool kPolyPairs = ROWS == 32;  // every other pair: one sub-partition's pipe serves all four warps
         const int part = ROWS == 32 ? warp / 4 : 0, row = ROWS == 32 ? lane : (int)threadIdx.x;
         const uint32_t lanes = ROWS == 32 ? 0u : (uint32_t)warp << 21, lead = lane == 0;
         const uint32_t ts = tmem + lanes + kCols * part, tp = tmem + kFColP + kCols / 2 * part + lanes;
@@ -596,12 +584,8 @@ __global__ void __launch_bounds__(FewSmem<ROWS>::kThreads, 1)
                     const int i = 16 * q + 2 * e;
                     float2 x = make_float2(__uint_as_float(s[i / 32][i % 32]), __uint_as_float(s[i / 32][i % 32 + 1]));
                     x = __fadd2_rn(x, nm);
-                    if (kPolyPairs && (e & 1)) {
-                        x = few_ex2_poly(x);  // (a NaN row has its other pairs' NaN)
-                    } else {
-                        x.x = few_ex2(x.x);
-                        x.y = few_ex2(x.y);
-                    }
+                    x.x = few_ex2(x.x);
+                    x.y = few_ex2(x.y);
                     sum[e & 1] = __fadd2_rn(sum[e & 1], x);
                     const __half2 hp = __floats2half2_rn(x.x, x.y);
                     p[q][e] = *reinterpret_cast<const uint32_t*>(&hp);

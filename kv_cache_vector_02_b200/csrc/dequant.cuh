@@ -33,12 +33,20 @@ inline LevelTable make_level_table(const Codebook& cb) {
     return t;
 }
 
+// Bytes of (x, y) picked by the low four nibbles of a selector whose nibbles are below 8.
+// (__byte_perm masks the selector first; lookups are bound by the pipe that the mask takes.)
+__device__ __forceinline__ uint32_t pick4(uint32_t x, uint32_t y, uint32_t sel) {
+    uint32_t r;
+    asm("prmt.b32 %0, %1, %2, %3;" : "=r"(r) : "r"(x), "r"(y), "r"(sel));
+    return r;
+}
+
 // The halves of codes 2i, 2i + 1 (i = 0..3) from eight nibbles below 8.
 __device__ __forceinline__ void lookup8(uint32_t nib, const LevelTable& t, uint32_t sign_a, uint32_t sign_b,
                                         uint32_t (&w)[4]) {
     const uint32_t up = nib >> 16;
-    const uint32_t la = __byte_perm(t.lo[0], t.lo[1], nib), ha = __byte_perm(t.hi[0], t.hi[1], nib) | sign_a;
-    const uint32_t lb = __byte_perm(t.lo[0], t.lo[1], up), hb = __byte_perm(t.hi[0], t.hi[1], up) | sign_b;
+    const uint32_t la = pick4(t.lo[0], t.lo[1], nib), ha = pick4(t.hi[0], t.hi[1], nib) | sign_a;
+    const uint32_t lb = pick4(t.lo[0], t.lo[1], up), hb = pick4(t.hi[0], t.hi[1], up) | sign_b;
     w[0] = __byte_perm(la, ha, 0x5140);
     w[1] = __byte_perm(la, ha, 0x7362);
     w[2] = __byte_perm(lb, hb, 0x5140);

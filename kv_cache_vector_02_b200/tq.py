@@ -114,6 +114,13 @@ def _stream(stream):
     return stream.cuda_stream
 
 
+def _current_device() -> int | None:
+    """torch's current CUDA device, None where torch has none in use."""
+    import sys
+    torch = sys.modules.get("torch")
+    return torch.cuda.current_device() if torch is not None and torch.cuda.is_available() else None
+
+
 class Context:
     """Owns one libtq context (tq_init / tq_destroy)."""
 
@@ -121,6 +128,7 @@ class Context:
         self.handle = handle
         self.head_dim, self.bits, self.seed, self.rotation, self.key_mode = head_dim, bits, seed, rotation, key_mode
         self._chunk = {}  # chunk bytes by kind, asked of the library once
+        self.device = _current_device()  # what tq_init bound the context to
 
     def __del__(self):
         h = getattr(self, "handle", None)
@@ -328,6 +336,12 @@ def _same_device(what: str, first, *others) -> int:
     return dev
 
 
+def _check_device(ctx: Context, what: str, dev: int):
+    if ctx.device is not None and dev >= 0 and dev != ctx.device:
+        raise TQError(TQ_ERR_INVALID_ARG, "%s: tensors on cuda:%d must be on the context's device, cuda:%d" % (
+            what, dev, ctx.device))
+
+
 def _stream_on(stream, dev: int) -> int:
     """The stream's handle; by default the current stream of device `dev`."""
     if stream is not None:
@@ -399,8 +413,9 @@ def tq_prompt_attention(ctx: Context, q, k, v, cu_seqlens, out, scale: float = 0
         raise TQError(TQ_ERR_INVALID_ARG, "%s: cu_seqlens must have B + 1 entries" % what)
     _expect(out, (T, Hq, 128), (torch.float16, torch.float32), what, "out")
     dev = _same_device(what, q, k, v, cu_seqlens, out)
+    _check_device(ctx, what, dev)
     _check(_lib.tq_prompt_attention(ctx.handle, q.data_ptr(), sq, k.data_ptr(), sk, v.data_ptr(), sv, T,
-                                    cu_seqlens.data_ptr(), B, Hq, Hkv, scale, out.data_ptr(),
+                                    cu_seqlens.data_ptr(), B, Hq, Hkv, float(scale), out.data_ptr(),
                                     1 if out.dtype is torch.float32 else 0, _stream_on(stream, dev)), what)
 
 
@@ -432,9 +447,10 @@ def tq_chunk_attention(ctx: Context, q, cu_q, k_cache, v_cache, block_table, seq
     _expect(out, (total_q, Hq, ctx.head_dim), (torch.float16, torch.float32), what, "out")
     _expect(workspace, (None,), (torch.uint8,), what, "workspace")
     dev = _same_device(what, q, cu_q, k_cache, v_cache, block_table, seq_lens, out, workspace)
+    _check_device(ctx, what, dev)
     _check(_lib.tq_chunk_attention(ctx.handle, q.data_ptr(), cu_q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
                                    k_cache.shape[0], block_table.data_ptr(), block_table.shape[1], seq_lens.data_ptr(),
-                                   B, total_q, Hq, Hkv, max_seq_len, scale, out.data_ptr(),
+                                   B, total_q, Hq, Hkv, int(max_seq_len), float(scale), out.data_ptr(),
                                    1 if out.dtype is torch.float32 else 0, workspace.data_ptr(), workspace.numel(),
                                    _stream_on(stream, dev)), what)
 

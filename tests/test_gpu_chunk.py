@@ -202,6 +202,32 @@ def test_chunk_bad_pages_and_lengths(orc):
         assert tq.tq_get_device_error(c.c) & tq.DEVERR_SEQLEN
 
 
+@pytest.mark.parametrize("nq,G", [(6, 4), (30, 4), (150, 4)])
+@pytest.mark.parametrize("val", [float("nan"), float("inf")])
+def test_chunk_norms_that_are_not_finite(orc, nq, G, val):
+    """A norm that is not finite, of a token among the new ones: the queries before it equal the
+    run without it to the bit, those from it on are not finite (a rotated value reaches every
+    coordinate); a bad gamma or key norm likewise."""
+    import torch
+    tq = _tq()
+    L, at = 300, 300 - nq // 2
+    c = Case(orc, [nq, 2], [L, 40], G, 1, seed=14)
+    ref = c.run()
+    slot = int(c.slots[0][at])
+    keep = c.kc.clone(), c.vc.clone()
+    for cache, off in ((c.vc, 16 * 64), (c.kc, 16 * 80), (c.kc, 16 * 84)):
+        cache[slot // 16, 0].view(torch.float32)[off // 4 + slot % 16] = val
+        out = c.run()
+        assert tq.tq_get_device_error(c.c) == 0
+        first = at - (L - nq)
+        assert torch.equal(out[:first], ref[:first]) and torch.equal(out[nq:], ref[nq:])
+        # (an infinite key scalar times a negative product is a score of -inf: weight 0, a finite row)
+        if cache is c.vc or math.isnan(val):
+            assert not bool(torch.isfinite(out[first:nq]).any())
+        c.kc.copy_(keep[0])
+        c.vc.copy_(keep[1])
+
+
 def test_chunk_rows_outside_and_empty_calls(orc):
     import torch
     tq = _tq()
@@ -218,7 +244,7 @@ def test_chunk_rows_outside_and_empty_calls(orc):
     assert tq.tq_launch_count() == n0
     need = tq.tq_chunk_workspace_bytes(c.c, 2, 26, 8, 2, 400)
     for bad in (dict(ws=torch.empty(need - 1, dtype=torch.uint8, device="cuda")), dict(scale=-1.0),
-                dict(scale=float("nan")), dict(out=c.q)):
+                dict(scale=float("nan")), dict(out=c.q), dict(k_cache=c.kc[:0], v_cache=c.vc[:0])):
         with pytest.raises(tq.TQError) as e:
             c.run(**bad)
         assert e.value.status == tq.TQ_ERR_INVALID_ARG
