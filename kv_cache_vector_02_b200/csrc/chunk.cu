@@ -8,11 +8,11 @@
 // (2 sigma - 1) gives it as a plain inner product), section "架构设计" (decompress).
 //
 // unpack_tc_kernel, one persistent CTA per SM, per (sequence, tile, kv head):
-//   warps 0-3  one thread per token: its packed codes and signs (loaded a tile ahead) become
+//   warps 0-7  two threads per token: its packed codes and signs (loaded a tile ahead) become
 //              fp16 levels and +-1 in registers and go to three swizzled operand tiles
-//   warp 8     D1 = C_k R^T, D2 = Sigma S, D3 = C_v R^T on tcgen05 (R, S resident in shared
+//   warp 12    D1 = C_k R^T, D2 = Sigma S, D3 = C_v R^T on tcgen05 (R, S resident in shared
 //              memory; S as it lies, N-major)
-//   warps 4-7  one thread per token: k = n_k D1 + gamma' D2, v = n_v D3, rounded to fp16,
+//   warps 8-11 one thread per token: k = n_k D1 + gamma' D2, v = n_v D3, rounded to fp16,
 //              staged and written by TMA
 // Decompressing once costs 156 + 512 bytes a (token, head) against the 156 of the packed
 // pages, but every further row tile then reads fp16 from L2 with no arithmetic, and the
@@ -42,7 +42,8 @@ using namespace sm100;
 
 constexpr int kUN = 128;
 constexpr uint32_t kUTile = 128 * kDim * 2, kUHalf = kUTile / 2;
-constexpr int kUThreads = 288;
+constexpr int kUThreads = 416;
+constexpr int kUWarpIssue = 12;
 constexpr uint32_t kUOffR = 0, kUOffS = kUTile;
 constexpr uint32_t kUOffA = 2 * kUTile;                 // C_k | Sigma | C_v
 constexpr uint32_t kUOffOut = kUOffA + 3 * kUTile;      // k | v
@@ -67,7 +68,8 @@ struct UnpackArgs {
     int Hkv, heads, head0;  // kv heads of the cache; of this launch
     ChunkLayout lk, lv;
     LevelTable tk, tv;
-    float n_scale, g_scale; // 1/sqrt(d), sqrt(pi/2)/d
+    float k_scale, v_scale; // 1/sqrt(d), times the level tables' scales
+    float g_scale;          // sqrt(pi/2)/d
     uint8_t* pages_ok;
     uint32_t* err;
 };
@@ -76,26 +78,6 @@ __device__ __forceinline__ void tma_store_3d(const void* tmap, uint32_t src, int
     asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(tmap),
                  "r"(src), "r"(x), "r"(y), "r"(z)
                  : "memory");
-}
-
-// One token's packed row: codes of W bits (16 W bytes) as words.
-template <int W>
-__device__ __forceinline__ void load_row(const uint8_t* p, uint32_t (&w)[4 * W]) {
-#pragma unroll
-    for (int i = 0; i < W; ++i) {
-        const uint4 x = *reinterpret_cast<const uint4*>(p + 16 * i);
-        w[4 * i] = x.x;
-        w[4 * i + 1] = x.y;
-        w[4 * i + 2] = x.z;
-        w[4 * i + 3] = x.w;
-    }
-}
-
-// The codes of coordinates 8c .. 8c + 7.
-template <int W>
-__device__ __forceinline__ uint32_t codes_of(const uint32_t (&w)[4 * W], int c) {
-    const int bit = 8 * W * c;
-    return w[bit / 32] >> (bit % 32);
 }
 
 template <int WK, int LK, bool PROD, int WV, int LV>
@@ -120,7 +102,7 @@ __global__ void __launch_bounds__(kUThreads, 1)
     };
     if (threadIdx.x == 0) {
         mbar_init(bar(kUBConst), 1);
-        mbar_init(bar(kUBA), 4);
+        mbar_init(bar(kUBA), 8);
         mbar_init(bar(kUBD), 1);
         mbar_init(bar(kUBDEmpty), 4);
         *abort = 0;
@@ -131,7 +113,7 @@ __global__ void __launch_bounds__(kUThreads, 1)
             if (PROD) tma_load_2d(sbase + kUOffS + x * kUHalf, &s_map, 64 * x, 0, bar(kUBConst));
         }
     }
-    if (warp == 8) {
+    if (warp == kUWarpIssue) {
         tmem_alloc(smem_u32(tmem_slot), 512);
         tmem_relinquish();
     }
@@ -169,25 +151,27 @@ __global__ void __launch_bounds__(kUThreads, 1)
         return cache + ((size_t)blk * a.Hkv + a.head0 + h) * lay.bytes;
     };
 
-    if (warp < 4) {
+    if (warp < 8) {
         // ------------------------------------------------------------ codes to operands
-        const int row = threadIdx.x, r16 = row % kPage;
-        uint32_t kw[4 * WK] = {}, vw[4 * WV] = {}, sw[4] = {};
+        const int row = threadIdx.x & 127, sub = warp >> 2, r16 = row % kPage;
+        PartRow<WK, 2> kw{};
+        PartRow<WV, 2> vw{};
+        PartRow<1, 2> sw{};
         auto fetch = [&](const Item& it) {
             const int blk = block_of(it, it.j * kUN + row);
             if (blk < 0) return;
             const uint8_t* kp = chunk(a.kc, a.lk, blk, it.h);
-            load_row<WK>(kp + r16 * a.lk.code_row, kw);
-            if (PROD) load_row<1>(kp + a.lk.signs_off + r16 * (kDim / 8), sw);
-            load_row<WV>(chunk(a.vc, a.lv, blk, it.h) + r16 * a.lv.code_row, vw);
+            kw.load(kp + r16 * a.lk.code_row + sub * 8 * WK);
+            if (PROD) sw.load(kp + a.lk.signs_off + r16 * (kDim / 8) + sub * 8);
+            vw.load(chunk(a.vc, a.lv, blk, it.h) + r16 * a.lv.code_row + sub * 8 * WV);
         };
         long long i = blockIdx.x;
         Item it;
         bool have = next(i, it);
         if (have) fetch(it);
-        uint8_t* tile = smem + kUOffA + row * 128;
+        uint8_t* tile = smem + kUOffA + row * 128 + sub * kUHalf;
         for (int k = 0; have; ++k) {
-            if (it.h == 0 && row == 0) {  // the tile's usable pages, once for all heads
+            if (it.h == 0 && threadIdx.x == 0) {  // the tile's usable pages, once for all heads
                 uint32_t m = 0;
                 for (int p = 0; p < kUN / kPage; ++p) {
                     const int t = it.j * kUN + p * kPage;
@@ -203,16 +187,16 @@ __global__ void __launch_bounds__(kUThreads, 1)
                 break;
             }
 #pragma unroll
-            for (int c = 0; c < 16; ++c) {
-                const uint32_t at = (c / 8) * kUHalf + (((c % 8) ^ (row & 7)) << 4);
+            for (int c = 0; c < 8; ++c) {
+                const uint32_t at = (uint32_t)(c ^ (row & 7)) << 4;
                 uint32_t w[4];
-                levels8<WK, LK>(codes_of<WK>(kw, c), a.tk, w);
+                levels8<WK, LK>(kw.codes(c), a.tk, w);
                 *reinterpret_cast<uint4*>(tile + at) = make_uint4(w[0], w[1], w[2], w[3]);
                 if (PROD) {
-                    signs8(codes_of<1>(sw, c), 0x3C003C00u, w);
+                    signs8(sw.codes(c), 0x3C003C00u, w);
                     *reinterpret_cast<uint4*>(tile + kUTile + at) = make_uint4(w[0], w[1], w[2], w[3]);
                 }
-                levels8<WV, LV>(codes_of<WV>(vw, c), a.tv, w);
+                levels8<WV, LV>(vw.codes(c), a.tv, w);
                 *reinterpret_cast<uint4*>(tile + 2 * kUTile + at) = make_uint4(w[0], w[1], w[2], w[3]);
             }
             fence_proxy_async_shared();
@@ -221,7 +205,7 @@ __global__ void __launch_bounds__(kUThreads, 1)
             have = next(i, it);
             if (have) fetch(it);
         }
-    } else if (warp == 8) {
+    } else if (warp == kUWarpIssue) {
         // ------------------------------------------------------------ MMA issuer
         // (the whole warp, converged: see umma_ss_warp; all 512 columns are ours, from 0 on)
         constexpr uint32_t id_k = idesc_f16(128, kDim), id_n = id_k | (1u << 16);
@@ -265,7 +249,7 @@ __global__ void __launch_bounds__(kUThreads, 1)
         __syncwarp();
     } else {
         // ------------------------------------------------------------ scale, round, store
-        const int row = threadIdx.x - 128, r16 = row % kPage;
+        const int row = threadIdx.x - 256, r16 = row % kPage;
         const uint32_t lanes = (uint32_t)(warp & 3) << 21;
         long long i = blockIdx.x;
         Item it;
@@ -277,9 +261,9 @@ __global__ void __launch_bounds__(kUThreads, 1)
             const int blk = block_of(it, it.j * kUN + row);
             if (blk >= 0) {
                 const uint8_t* kp = chunk(a.kc, a.lk, blk, it.h);
-                kn = reinterpret_cast<const float*>(kp + a.lk.norm_off)[r16] * a.n_scale;
+                kn = reinterpret_cast<const float*>(kp + a.lk.norm_off)[r16] * a.k_scale;
                 if (PROD) kg = reinterpret_cast<const float*>(kp + a.lk.gamma_off)[r16] * a.g_scale;
-                vn = reinterpret_cast<const float*>(chunk(a.vc, a.lv, blk, it.h) + a.lv.norm_off)[r16] * a.n_scale;
+                vn = reinterpret_cast<const float*>(chunk(a.vc, a.lv, blk, it.h) + a.lv.norm_off)[r16] * a.v_scale;
             }
             // the staging area is free (the copies of the item before have read it).  After a
             // wait that gave up the loop goes on without storing: the barrier needs every warp.
@@ -351,7 +335,7 @@ __global__ void __launch_bounds__(kUThreads, 1)
         if (row == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     }
     __syncthreads();
-    if (warp == 8) {
+    if (warp == kUWarpIssue) {
         tc_fence_after();
         tmem_dealloc(tmem, 512);
     }
@@ -505,9 +489,10 @@ cudaError_t launch_chunk(const tq_ctx* ctx, const ChunkPlan& plan, const ChunkCa
     u.Hkv = c.Hkv;
     u.lk = ctx->lay_key;
     u.lv = ctx->lay_value;
-    u.tk = make_level_table(ctx->cb_key);
-    u.tv = make_level_table(ctx->cb_value);
-    u.n_scale = 1.f / std::sqrt((float)kDim);
+    u.tk = ctx->levels_key;
+    u.tv = ctx->levels_value;
+    u.k_scale = u.tk.scale / std::sqrt((float)kDim);
+    u.v_scale = u.tv.scale / std::sqrt((float)kDim);
     u.g_scale = 1.2533141373155003f / (float)kDim;
     u.pages_ok = ws + plan.pages_off;
     u.err = ctx->dev_error;

@@ -11,17 +11,20 @@
 //                     (query, query head of the group) pair.  Per tile of 128 tokens:
 //   coding warps   two threads per token (32 rows: 16 warps, four per token) turn its packed
 //                  codes and signs, loaded two tiles ahead, into fp16 levels and +-1 in
-//                  registers, the values' times n_t/sqrt(d) (rounded to fp16, as decompressed
-//                  values are), and store them to swizzled operand tiles; a_t, b_t go to shared
-//                  memory
+//                  registers and store them to swizzled operand tiles; a_t, b_t and the values'
+//                  scalar v_t = n_t/sqrt(d) go to shared memory
 //   issuing warp   D1 = Q' C_k^T, D2 = S_q Sigma^T, O += P V on tcgen05
 //   softmax warps  one thread per row: s = a_t D1 + b_t D2 in fp32 (the score's two scalars are
-//                  never rounded), mask, running maximum and sum, P to tensor memory; with 32
-//                  rows four warps share a tile's tokens, 32 each
+//                  never rounded), mask, running maximum and sum, P to tensor memory.  With 32
+//                  rows four warps share a tile's tokens, 32 each, and P is the weight times
+//                  v_t: the maximum runs over s + log2 v_t, P = 2^(s + log2 v_t - m) <= 2^8
+//                  whatever the values' size, and the sum takes P / v_t.  One rounding to fp16
+//                  instead of three (P, v_t, v_t c); with 128 rows, whose scalars do not fit
+//                  beside the tiles, the values' tile holds v_t c
 // few_join_kernel     the splits joined, o = R acc / l in fp32
 //
-// Bound (32 sequences, 1 to 8 queries of 32 heads, about 3600 tokens each: 145 us, 1.0 TB/s of
-// pages; 137 of it in the attend kernel): the decoding.  A tile is about 8000 warp instructions
+// Bound (32 sequences, 1 to 8 queries of 32 heads, about 3600 tokens each: 146 us, 1.0 TB/s of
+// pages; 135 of it in the attend kernel): the decoding.  A tile is about 8000 warp instructions
 // of lookups, two thirds of them on the ALU pipe at half rate, on the three sub-partitions that
 // the softmax leaves; a capture has the ALU pipe at 45 % over the whole kernel, the tensor pipe
 // at 31 %, DRAM at 13 %.  The MMAs of a tile, 24 of 65 cycles whatever the rows, would allow
@@ -60,8 +63,10 @@ struct FewSmem {
     static constexpr uint32_t kOffQ = 0;                       // q' | s: two blocks each
     static constexpr uint32_t kOffK = 4 * kBlock;              // two buffers of C_k | Sigma
     static constexpr uint32_t kOffV = kOffK + 4 * kFTile;      // C_v n / sqrt(d)
-    static constexpr uint32_t kOffScal = kOffV + kVBufs * kFTile;  // float [2][2][128]: a_t, b_t
-    static constexpr uint32_t kOffBar = kOffScal + 2 * 2 * 128 * 4;
+    static constexpr uint32_t kOffScal = kOffV + kVBufs * kFTile;  // float [2][kScalars][128]
+    static constexpr bool kWeighted = ROWS == 32;              // P carries the values' scalar (below)
+    static constexpr int kScalars = kWeighted ? 4 : 2;
+    static constexpr uint32_t kOffBar = kOffScal + 2 * kScalars * 128 * 4;
     static constexpr uint32_t kOffTop = kOffBar + 256;         // float [4][32] (ROWS = 32)
     static constexpr uint32_t kBytes = kOffTop + (ROWS == 32 ? 512 : 0);
     static_assert(kBytes <= 232448, "shared memory budget");
@@ -97,8 +102,8 @@ struct FewArgs {
     int Hq, Hkv, G, QT;      // QT = ROWS / G queries per CTA
     ChunkLayout lk, lv;
     LevelTable tk, tv;
-    float qscale, sscale;    // scale log2(e) / sqrt(d), scale log2(e) sqrt(pi/2) / d
-    float vscale;            // 1 / sqrt(d)
+    float qscale, sscale;    // scale log2(e) / sqrt(d) (times the key levels' scale), scale log2(e) sqrt(pi/2) / d
+    float vscale;            // 1 / sqrt(d) times the value levels' scale
     float* part;             // [splits][total_q * Hq][128] unscaled sums, rotated
     float2* ml;              // [splits][total_q * Hq] maximum (base 2) and sum
     void* out;               // rows of sequences with impossible lengths are zeroed here
@@ -129,48 +134,6 @@ __device__ __forceinline__ bool any_of_threads(int id, int n, bool x) {
     return r != 0;
 }
 __device__ __forceinline__ void sync_threads(int id, int n) { asm volatile("barrier.sync %0, %1;" ::"r"(id), "r"(n) : "memory"); }
-
-// One of SUB equal parts of a row of packed codes of W bits: 16 W / SUB bytes.
-template <int W, int SUB>
-struct PartRow {
-    static constexpr int kWords = 4 * W / SUB;
-    uint32_t w[kWords];
-    __device__ __forceinline__ void load(const uint8_t* p) {
-        if (kWords % 4 == 0) {
-#pragma unroll
-            for (int i = 0; i < kWords / 4; ++i) {
-                const uint4 x = reinterpret_cast<const uint4*>(p)[i];
-                w[4 * i] = x.x;
-                w[(4 * i + 1) % kWords] = x.y;
-                w[(4 * i + 2) % kWords] = x.z;
-                w[(4 * i + 3) % kWords] = x.w;
-            }
-        } else if (kWords == 2) {
-            const uint2 x = *reinterpret_cast<const uint2*>(p);
-            w[0] = x.x;
-            w[1 % kWords] = x.y;
-        } else {
-            w[0] = *reinterpret_cast<const uint32_t*>(p);
-        }
-    }
-    // Exchanges piece c with piece c ^ (kSub == 4 ? 2 : 4) of the part.
-    __device__ __forceinline__ void exchange(bool yes) {
-        constexpr int kStep = SUB == 4 ? W / 2 : W;  // words from one to the other
-        if (kStep == 0) {                            // (in one word)
-            w[0] = yes ? __byte_perm(w[0], 0u, 0x1032) : w[0];
-        } else {
-#pragma unroll
-            for (int i = 0; i < kWords; ++i)
-                if (!(i & (kStep ? kStep : 1))) {
-                    const uint32_t x = w[i], y = w[(i + kStep) % kWords];
-                    w[i] = yes ? y : x;
-                    w[(i + kStep) % kWords] = yes ? x : y;
-                }
-        }
-    }
-    // the codes of the part's coordinates 8c .. 8c + 7
-    __device__ __forceinline__ uint32_t codes(int c) const { return w[8 * W * c / 32] >> (8 * W * c % 32); }
-};
 
 template <int ROWS, int WK, int LK, bool PROD, int WV, int LV>
 __global__ void __launch_bounds__(FewSmem<ROWS>::kThreads, 1)
@@ -333,9 +296,16 @@ __global__ void __launch_bounds__(FewSmem<ROWS>::kThreads, 1)
                 }
             }
             if (sub == 0) {
-                float* scal = reinterpret_cast<float*>(smem + M::kOffScal) + s * 256 + tok;
+                float* scal = reinterpret_cast<float*>(smem + M::kOffScal) + s * (M::kScalars * 128) + tok;
                 scal[0] = r.state ? 0.f : r.kn * a.qscale;
                 if (PROD) scal[128] = r.state ? 0.f : r.kg * a.sscale;
+                if (M::kWeighted) {
+                    // (a zero value's 2^-100 keeps its weight in the sum and is 0 in P)
+                    const float v = fmaxf(fabsf(r.vn * a.vscale), 7.8886090522101181e-31f);
+                    const bool use = r.state == 0 && v < INFINITY;
+                    scal[256] = use ? __log2f(v) : 0.f;
+                    scal[384] = use ? __fdividef(1.f, v) : 0.f;
+                }
                 if (r16 == 0) {
                     page_bad[8 * s + tok / kPage] = r.state == 2;
                     if (r.state == 2) atomicOr(a.err, TQ_DEVERR_BLOCK);
@@ -363,7 +333,7 @@ __global__ void __launch_bounds__(FewSmem<ROWS>::kThreads, 1)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const __half2 x = __hmul2(*reinterpret_cast<const __half2*>(&w[i]), v2);
-                    w[i] = *reinterpret_cast<const uint32_t*>(&x);
+                    if (!M::kWeighted) w[i] = *reinterpret_cast<const uint32_t*>(&x);
                 }
                 *reinterpret_cast<uint4*>(vt + ((uint32_t)((piece0 + c) ^ swap ^ (tok & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
             }
@@ -476,7 +446,7 @@ __global__ void __launch_bounds__(FewSmem<ROWS>::kThreads, 1)
             wait(kFBS, j);
             tc_fence_after();
             uint32_t s[kChunks][32];
-            const float4* sc = reinterpret_cast<const float4*>(smem + M::kOffScal + (j & 1) * 1024) + kCols / 4 * part;
+            const float4* sc = reinterpret_cast<const float4*>(smem + M::kOffScal + (j & 1) * (M::kScalars * 512)) + kCols / 4 * part;
 #pragma unroll
             for (int q = 0; q < 2 * kChunks; ++q) {  // 16 tokens
                 uint32_t d1[16], d2[16];
@@ -488,8 +458,12 @@ __global__ void __launch_bounds__(FewSmem<ROWS>::kThreads, 1)
                     const float4 fa = sc[4 * q + e];
                     uint32_t* x = &s[q / 2][16 * (q & 1) + 4 * e];
                     const uint32_t* z = &d1[4 * e];
-                    float2 u = __fmul2_rn(make_float2(fa.x, fa.y), make_float2(__uint_as_float(z[0]), __uint_as_float(z[1])));
-                    float2 v = __fmul2_rn(make_float2(fa.z, fa.w), make_float2(__uint_as_float(z[2]), __uint_as_float(z[3])));
+                    // (-0: nothing added)
+                    const float4 fl = M::kWeighted ? sc[64 + 4 * q + e] : make_float4(-0.f, -0.f, -0.f, -0.f);
+                    const float2 z01 = make_float2(__uint_as_float(z[0]), __uint_as_float(z[1]));
+                    const float2 z23 = make_float2(__uint_as_float(z[2]), __uint_as_float(z[3]));
+                    float2 u = __ffma2_rn(make_float2(fa.x, fa.y), z01, make_float2(fl.x, fl.y));
+                    float2 v = __ffma2_rn(make_float2(fa.z, fa.w), z23, make_float2(fl.z, fl.w));
                     if (PROD) {
                         const float4 fb = sc[32 + 4 * q + e];
                         const uint32_t* y = &d2[4 * e];
@@ -505,7 +479,7 @@ __global__ void __launch_bounds__(FewSmem<ROWS>::kThreads, 1)
             const uint2 pb = *reinterpret_cast<const uint2*>(page_bad + 8 * (j & 1));
             tc_fence_before();
             mbar_arrive_lead(lead, bar(kFBL));
-            mbar_arrive_lead(lead, bar(kFBKEmpty + (j & 1)));
+            if (!M::kWeighted) mbar_arrive_lead(lead, bar(kFBKEmpty + (j & 1)));
             if (j >= masked_from) {
                 const int lim = limit - j * kFN - kCols * part;
 #pragma unroll
@@ -586,11 +560,17 @@ __global__ void __launch_bounds__(FewSmem<ROWS>::kThreads, 1)
                     x = __fadd2_rn(x, nm);
                     x.x = few_ex2(x.x);
                     x.y = few_ex2(x.y);
-                    sum[e & 1] = __fadd2_rn(sum[e & 1], x);
+                    if (M::kWeighted) {  // the weight in the sum is without the value's scalar
+                        const float2 iv = reinterpret_cast<const float2*>(sc + 96)[8 * q + e];
+                        sum[e & 1] = __ffma2_rn(x, iv, sum[e & 1]);
+                    } else {
+                        sum[e & 1] = __fadd2_rn(sum[e & 1], x);
+                    }
                     const __half2 hp = __floats2half2_rn(x.x, x.y);
                     p[q][e] = *reinterpret_cast<const uint32_t*>(&hp);
                 }
             }
+            if (M::kWeighted) mbar_arrive_lead(lead, bar(kFBKEmpty + (j & 1)));  // its scalars are read
             // the tile before's P has been read
             if (j > 0 && !any) wait(kFBO, j - 1);
 #pragma unroll
@@ -862,11 +842,11 @@ cudaError_t launch_chunk_few(const tq_ctx* ctx, const ChunkPlan& plan, const Chu
     a.QT = plan.rows / a.G;
     a.lk = ctx->lay_key;
     a.lv = ctx->lay_value;
-    a.tk = make_level_table(ctx->cb_key);
-    a.tv = make_level_table(ctx->cb_value);
+    a.tk = ctx->levels_key;
+    a.tv = ctx->levels_value;
     const float scale_log2 = c.scale * 1.4426950408889634f;
-    a.vscale = 1.f / std::sqrt((float)kDim);
-    a.qscale = scale_log2 * a.vscale;
+    a.vscale = a.tv.scale / std::sqrt((float)kDim);
+    a.qscale = scale_log2 * a.tk.scale / std::sqrt((float)kDim);
     a.sscale = scale_log2 * 1.2533141373155003f / (float)kDim;
     a.part = reinterpret_cast<float*>(ws + plan.part_off);
     a.ml = reinterpret_cast<float2*>(ws + plan.ml_off);

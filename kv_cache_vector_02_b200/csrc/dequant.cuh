@@ -14,24 +14,47 @@
 
 namespace tq {
 
-// fp16 levels by byte: lo[0] byte j = low byte of level j, and so on (filled on the host).
-struct LevelTable {
-    uint32_t lo[2], hi[2];
-};
-
-inline LevelTable make_level_table(const Codebook& cb) {
-    LevelTable t{};
-    // 16 levels: the positive half, c[8 + j]; 2 levels: the positive one
-    const int n = cb.levels == 16 ? 8 : cb.levels == 2 ? 1 : cb.levels;
-    for (int j = 0; j < n; ++j) {
-        const __half h = __float2half_rn(cb.c[cb.levels == 16 ? 8 + j : cb.levels == 2 ? 1 : j]);
-        uint16_t u;
-        __builtin_memcpy(&u, &h, 2);
-        t.lo[j / 4] |= uint32_t(u & 0xff) << (8 * (j % 4));
-        t.hi[j / 4] |= uint32_t(u >> 8) << (8 * (j % 4));
+// One of SUB equal parts of a row of packed codes of W bits: 16 W / SUB bytes.
+template <int W, int SUB>
+struct PartRow {
+    static constexpr int kWords = 4 * W / SUB;
+    uint32_t w[kWords];
+    __device__ __forceinline__ void load(const uint8_t* p) {
+        if (kWords % 4 == 0) {
+#pragma unroll
+            for (int i = 0; i < kWords / 4; ++i) {
+                const uint4 x = reinterpret_cast<const uint4*>(p)[i];
+                w[4 * i] = x.x;
+                w[(4 * i + 1) % kWords] = x.y;
+                w[(4 * i + 2) % kWords] = x.z;
+                w[(4 * i + 3) % kWords] = x.w;
+            }
+        } else if (kWords == 2) {
+            const uint2 x = *reinterpret_cast<const uint2*>(p);
+            w[0] = x.x;
+            w[1 % kWords] = x.y;
+        } else {
+            w[0] = *reinterpret_cast<const uint32_t*>(p);
+        }
     }
-    return t;
-}
+    // Exchanges piece c with piece c ^ (SUB == 4 ? 2 : 4) of the part.
+    __device__ __forceinline__ void exchange(bool yes) {
+        constexpr int kStep = SUB == 4 ? W / 2 : W;  // words from one to the other
+        if (kStep == 0) {                            // (in one word)
+            w[0] = yes ? __byte_perm(w[0], 0u, 0x1032) : w[0];
+        } else {
+#pragma unroll
+            for (int i = 0; i < kWords; ++i)
+                if (!(i & (kStep ? kStep : 1))) {
+                    const uint32_t x = w[i], y = w[(i + kStep) % kWords];
+                    w[i] = yes ? y : x;
+                    w[(i + kStep) % kWords] = yes ? x : y;
+                }
+        }
+    }
+    // the codes of the part's coordinates 8c .. 8c + 7
+    __device__ __forceinline__ uint32_t codes(int c) const { return w[8 * W * c / 32] >> (8 * W * c % 32); }
+};
 
 // Bytes of (x, y) picked by the low four nibbles of a selector whose nibbles are below 8.
 // (__byte_perm masks the selector first; lookups are bound by the pipe that the mask takes.)

@@ -19,6 +19,34 @@ namespace {
 std::atomic<uint64_t> g_launches{0};
 }
 
+tq::LevelTable tq::make_level_table(const Codebook& cb) {
+    const int n = cb.levels == 16 ? 8 : cb.levels == 2 ? 1 : cb.levels;
+    const float* c = cb.c + (cb.levels == 16 ? 8 : cb.levels == 2 ? 1 : 0);
+    double best = 1e300, factor = 1.0;
+    for (int i = 0; i < 4096; ++i) {
+        const double f = 1.0 + i / 4096.0;
+        double e = 0.0;
+        for (int j = 0; j < n; ++j) {
+            const double x = c[j] * f, d = double(__half2float(__double2half(x))) / x - 1.0;
+            e += d * d;
+        }
+        if (e < best) {
+            best = e;
+            factor = f;
+        }
+    }
+    LevelTable t{};
+    t.scale = float(1.0 / factor);
+    for (int j = 0; j < n; ++j) {
+        const __half h = __double2half(c[j] * factor);
+        uint16_t u;
+        std::memcpy(&u, &h, 2);
+        t.lo[j / 4] |= uint32_t(u & 0xff) << (8 * (j % 4));
+        t.hi[j / 4] |= uint32_t(u >> 8) << (8 * (j % 4));
+    }
+    return t;
+}
+
 void tq::count_launches(unsigned n) { g_launches.fetch_add(n, std::memory_order_relaxed); }
 
 bool tq::take_stall(const tq_ctx* ctx) {
@@ -178,6 +206,8 @@ static void fill_host(tq_ctx* ctx, int head_dim, int bits, uint64_t seed, int ro
     const tq::HostParams& H = ctx->host;
     ctx->cb_value = make_codebook(H.cv, H.tv, H.vbits);
     ctx->cb_key = make_codebook(H.ck, H.tk, H.kbits);
+    ctx->levels_value = tq::make_level_table(ctx->cb_value);
+    ctx->levels_key = tq::make_level_table(ctx->cb_key);
     ctx->lay_value = make_layout(H.vbits, false);
     ctx->lay_key = make_layout(H.kbits, key_mode == TQ_KEY_PROD);
 }

@@ -42,6 +42,16 @@ struct Codebook {
     int levels;               // 2^bits
 };
 
+// fp16 levels by byte, for register lookups (dequant.cuh): lo[0] byte j = low byte of level j,
+// and so on; 16 levels: the 8 positive ones, 2 levels: the positive one.  They are the
+// codebook's times a common factor, 1 to 2, that rounds them best to fp16 (by 4096 steps: 3 to
+// 20 times closer than the levels themselves); `scale` undoes it.
+struct LevelTable {
+    uint32_t lo[2], hi[2];
+    float scale;
+};
+LevelTable make_level_table(const Codebook& cb);
+
 // Byte geometry of one 16-token chunk.
 struct ChunkLayout {
     int code_row;     // bytes of packed codes per token (d * width / 8)
@@ -85,6 +95,7 @@ struct tq_ctx {
     int sm_count = 0;
     tq::HostParams host;
     tq::Codebook cb_value{}, cb_key{};
+    tq::LevelTable levels_value{}, levels_key{};
     tq::ChunkLayout lay_value{}, lay_key{};
     tq::DeviceParams dev{};
     tq::TcTables tc{};              // tensor-core compress operands and tables (in dev_block)
