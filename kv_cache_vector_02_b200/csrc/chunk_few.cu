@@ -266,7 +266,7 @@ __global__ void __launch_bounds__(FewSmem<ROWS>::kThreads, 1)
             if (PROD) r.kg = reinterpret_cast<const float*>(kp + a.lk.gamma_off)[r16];
             r.vn = reinterpret_cast<const float*>(vp + a.lv.norm_off)[r16];
         };
-                // 16-byte pieces c = sub * kPer .. of the row, at c ^ (row % 8) within their half
+        // 16-byte pieces c = sub * kPer .. of the row, at c ^ (row % 8) within their half
         constexpr int kPer = 16 / kSub;
         const uint32_t row = (uint32_t)tok * 128 + (sub * kPer / 8) * kFHalf;
         const int piece0 = sub * kPer % 8;

@@ -56,6 +56,12 @@ struct Unit {
 // Interleaved: unit u holds values [8u, 8u+8).
 // VEC = 1 (half layout whose rot/2 is no multiple of 8): unit u < rot/2 holds one pair, the
 // others one value.
+// Place of pair p's (cos, sin): the lanes of a head read theirs side by side.
+template <bool HALF, int VEC>
+__device__ __forceinline__ int place(int p) {
+    return VEC == 1 ? p : HALF ? (p & 7) * 8 + (p >> 3) : (p & 3) * 16 + (p >> 2);
+}
+
 template <bool HALF, int VEC>
 __global__ void __launch_bounds__(kRThreads) rope_kernel(const __grid_constant__ RopeArgs a) {
     __shared__ float2 cs[kRTokens][kDim / 2];
@@ -107,7 +113,7 @@ __global__ void __launch_bounds__(kRThreads) rope_kernel(const __grid_constant__
                 const uint64_t f = (uint64_t)(int64_t)pos * a.tab.turns[p] + (1ull << 31);
                 float s, c;
                 sincospif((float)(int32_t)(f >> 32) * 4.656612873077393e-10f /* 2^-31 */, &s, &c);
-                cs[t][p] = make_float2(c * a.m, s * a.ms);
+                cs[t][place<HALF, VEC>(p)] = make_float2(c * a.m, s * a.ms);
                 if (p == 0) live[t] = pos >= 0;
             }
             __syncthreads();
@@ -128,7 +134,7 @@ __global__ void __launch_bounds__(kRThreads) rope_kernel(const __grid_constant__
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
                         const float2 x1 = __half22float2(p[j]), x2 = __half22float2(p2[j]);
-                        const float2 w0 = w[8 * l + 2 * j], w1 = w[8 * l + 2 * j + 1];
+                        const float2 w0 = w[place<HALF, VEC>(8 * l + 2 * j)], w1 = w[place<HALF, VEC>(8 * l + 2 * j + 1)];
                         p[j] = __floats2half2_rn(x1.x * w0.x - x2.x * w0.y, x1.y * w1.x - x2.y * w1.y);
                         p2[j] = __floats2half2_rn(x2.x * w0.x + x1.x * w0.y, x2.y * w1.x + x1.y * w1.y);
                     }
@@ -136,7 +142,7 @@ __global__ void __launch_bounds__(kRThreads) rope_kernel(const __grid_constant__
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
                         if (8 * l + 2 * j < rot) {
-                            const float2 v = __half22float2(p[j]), wj = w[4 * l + j];
+                            const float2 v = __half22float2(p[j]), wj = w[place<HALF, VEC>(4 * l + j)];
                             p[j] = __floats2half2_rn(v.x * wj.x - v.y * wj.y, v.y * wj.x + v.x * wj.y);
                         }
                     }
