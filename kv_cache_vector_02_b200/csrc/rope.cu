@@ -15,10 +15,12 @@
 // half layout, 8 values in the interleaved one), then one thread per (token, pair) puts
 // (cos, sin) into shared memory, and after one barrier every head of the token uses them.
 // Computing them per head instead costs Hq + Hkv times the sincospif work.
-// 32768 tokens of 72 heads: 196 us, 6.16 TB/s (96 % of the measured copy).  Many small blocks
-// carry it, their barriers and their loads at different times: blocks of 256 threads with four
-// units took 265 us, of 512 with two 331, of 128 with five 246; a division per unit by a
-// runtime number (now a multiplication) cost another 20.
+// 32768 tokens of 72 heads: 186 us, 6.5 TB/s, the measured copy's rate.  Many small blocks carry
+// it, their barriers and their loads at different times (before the layout of `place`: 196 us;
+// 265 with blocks of 256 threads and four units, 331 with 512 and two, 246 with 128 and five); a
+// division per unit by a runtime number, now a multiplication, cost another 20.  4099 tokens of
+// 40 heads, half of each rotated: 20 us, 4.1 TB/s, of which about 8 are the launch and the tail
+// (four units a thread: 22.5).
 #include <cuda_fp16.h>
 
 #include "tq_internal.h"
