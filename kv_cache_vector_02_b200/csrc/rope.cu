@@ -16,10 +16,10 @@
 // (cos, sin) into shared memory, and after one barrier every head of the token uses them.
 // Computing them per head instead costs Hq + Hkv times the sincospif work.
 // 32768 tokens of 72 heads: 186 us, 6.5 TB/s, the measured copy's rate.  Many small blocks carry
-// it, their barriers and their loads at different times (before the layout of `place`: 196 us;
+// it, their barriers and their loads at different times (before (cos, sin) lay in the lanes' order: 196 to 215 us;
 // 265 with blocks of 256 threads and four units, 331 with 512 and two, 246 with 128 and five); a
 // division per unit by a runtime number, now a multiplication, cost another 20.  4099 tokens of
-// 40 heads, half of each rotated: 20 us, 4.1 TB/s, of which about 8 are the launch and the tail
+// 40 heads, half of each rotated: 20 us, 4.1 TB/s, against 13 for its bytes
 // (four units a thread: 22.5).
 #include <cuda_fp16.h>
 
