@@ -554,6 +554,8 @@ tq_status tq_prompt_attention(const tq_ctx* ctx, const uint16_t* q, int64_t q_st
     if (overlap(o, fp16_rows(q, T, Hq, q_stride)) || overlap(o, fp16_rows(k, T, Hkv, k_stride)) ||
         overlap(o, fp16_rows(v, T, Hkv, v_stride)))
         return TQ_ERR_INVALID_ARG;
+    const long long list_bytes = ((long long)B + 1) * 4;
+    if (overlap(o, Rows{cu_seqlens, 1, list_bytes, list_bytes})) return TQ_ERR_INVALID_ARG;
     if (scale == 0.f) scale = 1.0f / std::sqrt(float(kDim));
     DeviceGuard dev(ctx->device);
     if (!dev.ok) return TQ_ERR_CUDA;

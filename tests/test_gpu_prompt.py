@@ -199,6 +199,19 @@ def test_prompt_bad_lists_and_empty_calls():
         tq.tq_prompt_attention(ctx, q, k, v, _starts([100]), q)
 
 
+def test_prompt_refuses_output_over_the_list():
+    import torch
+    tq = _tq()
+    ctx = gpu_ctx()
+    q, k, v = _inputs(8, 2, 1, 15)
+    out = torch.zeros_like(q)
+    cu = out.view(-1).view(torch.int32)[:2]
+    cu.copy_(_starts([8]))
+    with pytest.raises(tq.TQError):
+        tq.tq_prompt_attention(ctx, q, k, v, cu, out)
+    assert cu.tolist() == [0, 8] and not out.view(-1)[4:].any()
+
+
 def test_prompt_streams_graphs_and_repeats():
     """The same bits on another stream, in a captured and replayed graph, and every time."""
     import torch
