@@ -26,8 +26,8 @@
 // Bound (32 sequences, 1 to 8 queries of 32 heads, about 3600 tokens each: 146 us, 1.0 TB/s of
 // pages; 135 of it in the attend kernel): the decoding.  A tile is about 8000 warp instructions
 // of lookups, two thirds of them on the ALU pipe at half rate, on the three sub-partitions that
-// the softmax leaves; a capture has the ALU pipe at 45 % over the whole kernel, the tensor pipe
-// at 31 %, DRAM at 13 %.  The MMAs of a tile, 24 of 65 cycles whatever the rows, would allow
+// the softmax leaves; a capture has the ALU pipe at 52 % over the whole kernel, the tensor pipe
+// at 38 %, DRAM at 13 %.  The MMAs of a tile, 24 of 65 cycles whatever the rows, would allow
 // 1560 cycles where it takes about 4000.  On the way: decompressing to fp16 first, 305 us; one
 // register set and one value buffer, 255; two of each up to 32 rows, 171; four softmax warps, 145.
 // Tried: four copies of the rows, one per lane quarter, each with its own softmax warp and a
@@ -700,10 +700,11 @@ struct JoinArgs {
     void* out;
     int out_fp32;
 };
-constexpr int kJoinThreads = 256, kJoinPer = 2, kJoinRows = 8 * kJoinPer;
-constexpr uint32_t kJoinSmem = kDim * kDim * 4 + kJoinRows * kDim * 4;
+constexpr uint32_t join_smem(int rows) { return kDim * kDim * 4 + rows * kDim * 4; }
 
-__global__ void __launch_bounds__(kJoinThreads) few_join_kernel(const JoinArgs a) {
+template <int WARPS, int PER>
+__global__ void __launch_bounds__(32 * WARPS) few_join_kernel(const JoinArgs a) {
+    constexpr int kJoinThreads = 32 * WARPS, kJoinPer = PER, kJoinRows = WARPS * PER;
     extern __shared__ __align__(16) uint8_t smem[];
     const uint32_t base = smem_u32(smem);
     for (int i = threadIdx.x; i < kDim * kDim / 4; i += kJoinThreads) cp_async16(base + 16 * i, a.RT + 4 * i);
@@ -802,6 +803,30 @@ cudaError_t launch_after(void (*k)(P...), dim3 grid, int threads, uint32_t smem,
     return e;
 }
 
+template <int WARPS, int PER>
+cudaError_t launch_join_shape(const JoinArgs& m, long long rows, cudaStream_t stream) {
+    auto k = few_join_kernel<WARPS, PER>;
+    static std::atomic<uint64_t> ready{0};
+    const cudaError_t e = ready_kernel(k, ready, (int)join_smem(WARPS * PER));
+    if (e != cudaSuccess) return e;
+    const long long blocks = (rows + WARPS * PER - 1) / (WARPS * PER);
+    return launch_after(k, dim3((unsigned)blocks), 32 * WARPS, join_smem(WARPS * PER), stream, m);
+}
+
+// Every warp reads the whole matrix (64 KB) from shared memory, so a block takes as long as it
+// has warps, and fetches it once whatever their number: the fewest rows per block that keep the
+// grid within two blocks per SM.  The whole call in us, with 2 x 1 / 4 x 1 / 4 x 2 / 8 x 2
+// (warps x rows): 512 rows 19.6 / 21.3 / 22.7 / 27.1; 1024 rows 35.0 / 33.4 / 34.9 / 39.3;
+// 2048 rows - / 62.8 / 59.6 / 63.8; 4096 rows - / 47.1 / 43.1 / 42.2 (300 cached
+// tokens a sequence; the first three of 1 query each, the last of 4).
+cudaError_t launch_join(const JoinArgs& m, long long rows, cudaStream_t stream) {
+    const long long per_block = (rows + 2 * 148 - 1) / (2 * 148);
+    if (per_block <= 2) return launch_join_shape<2, 1>(m, rows, stream);
+    if (per_block <= 4) return launch_join_shape<4, 1>(m, rows, stream);
+    if (per_block <= 8) return launch_join_shape<4, 2>(m, rows, stream);
+    return launch_join_shape<8, 2>(m, rows, stream);
+}
+
 template <int ROWS, int WK, int LK, bool PROD, int WV, int LV>
 cudaError_t launch_few_attend(const CUtensorMap& q, const FewArgs& a, dim3 grid, cudaStream_t stream) {
     auto k = few_attend_kernel<ROWS, WK, LK, PROD, WV, LV>;
@@ -887,11 +912,7 @@ cudaError_t launch_chunk_few(const tq_ctx* ctx, const ChunkPlan& plan, const Chu
     m.RT = ctx->dev.RT;
     m.out = c.out;
     m.out_fp32 = c.out_fp32;
-    static std::atomic<uint64_t> ready{0};
-    e = ready_kernel(few_join_kernel, ready, (int)kJoinSmem);
-    if (e != cudaSuccess) return e;
-    const long long blocks = (rows + kJoinRows - 1) / kJoinRows;
-    return launch_after(few_join_kernel, dim3((unsigned)blocks), kJoinThreads, kJoinSmem, stream, m);
+    return launch_join(m, rows, stream);
 }
 
 }  // namespace tq
