@@ -140,15 +140,15 @@ __global__ void __launch_bounds__(kAThreads, 1)
                 atomicOr(a.err, TQ_DEVERR_SEQLEN);
     }
     const int b = find_tile_seq(a.cu_q, a.B, QC, slot, lane);
-    const int c0 = a.cu_q[b], nq = a.cu_q[b + 1] - c0;
-    if (c0 < 0 || nq <= 0 || c0 + nq > a.total_q) return;
+    const int c0 = a.cu_q[b], c1 = a.cu_q[b + 1];
+    if (c0 < 0 || c1 <= c0 || c1 > a.total_q) return;  // (entry by entry: differences of any two may overflow)
+    const int nq = c1 - c0;
     const int tiles = (nq + QC - 1) / QC;
     const int rank = slot - (c0 / QC + b);
     if (rank < 0 || rank >= tiles) return;
     const int q0 = (tiles - 1 - rank) * QC;  // this CTA's first query; the sequence's heaviest tile first
     const int kv_len = a.kv_lens ? a.kv_lens[b] : nq;
-    const int off = kv_len - nq;
-    if (off < 0 || (a.kv_lens && kv_len > a.max_kv)) {  // a length that cannot be: zero rows
+    if (kv_len < nq || (a.kv_lens && kv_len > a.max_kv)) {  // a length that cannot be: zero rows
         if (blockIdx.y) return;
         if (threadIdx.x == 0) atomicOr(a.err, TQ_DEVERR_SEQLEN);
         const int rows = min(QC, nq - q0) * a.G;
@@ -160,6 +160,7 @@ __global__ void __launch_bounds__(kAThreads, 1)
         }
         return;
     }
+    const int off = kv_len - nq;
     // tiles of each half: up to its last query's position
     auto tiles_of = [&](int h) {
         const int first = q0 + h * a.QT;

@@ -155,14 +155,15 @@ __global__ void __launch_bounds__(FewSmem<ROWS>::kThreads, 1)
                 atomicOr(a.err, TQ_DEVERR_SEQLEN);
     }
     const int b = find_tile_seq(a.cu_q, a.B, a.QT, slot, lane);
-    const int c0 = a.cu_q[b], nq = a.cu_q[b + 1] - c0;
-    if (c0 < 0 || nq <= 0 || c0 + nq > a.total_q) return;
+    const int c0 = a.cu_q[b], c1 = a.cu_q[b + 1];
+    if (c0 < 0 || c1 <= c0 || c1 > a.total_q) return;  // (entry by entry: differences of any two may overflow)
+    const int nq = c1 - c0;
     const int rank = slot - (c0 / a.QT + b);
     if (rank < 0 || rank >= (nq + a.QT - 1) / a.QT) return;
     const int q0 = rank * a.QT, nrows = min(a.QT, nq - q0) * a.G;
-    const int kv_len = a.seq_lens[b], off = kv_len - nq;
+    const int kv_len = a.seq_lens[b];
     auto out_row = [&](int r) { return (size_t)(c0 + q0 + r / a.G) * a.Hq + hk * a.G + r % a.G; };
-    if (off < 0 || kv_len > a.max_kv) {  // a length that cannot be: zero rows
+    if (kv_len < nq || kv_len > a.max_kv) {  // a length that cannot be: zero rows
         if (blockIdx.y) return;
         if (threadIdx.x == 0) atomicOr(a.err, TQ_DEVERR_SEQLEN);
         for (int i = threadIdx.x; i < nrows * kDim; i += M::kThreads) {
@@ -173,6 +174,7 @@ __global__ void __launch_bounds__(FewSmem<ROWS>::kThreads, 1)
         return;
     }
     // this split's tiles: j0 .. j0 + n - 1, up to the last query's position
+    const int off = kv_len - nq;
     const int last = off + min(q0 + a.QT, nq);  // tokens that its last query attends
     const int all = (last + kFN - 1) / kFN;
     const int share = (all + (int)gridDim.y - 1) / (int)gridDim.y, j0 = min((int)blockIdx.y * share, all);

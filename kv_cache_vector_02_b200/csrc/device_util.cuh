@@ -44,7 +44,8 @@ __device__ __forceinline__ int find_last(int B, int s, int lane, Key key) {
 // floor(cu[b] / q) + b on.  (Its ceil(n_b / q) tiles fit before the next one's: floor((c + n) / q)
 // + 1 >= floor(c / q) + ceil(n / q).)  The sequence of slot s:
 __device__ __forceinline__ int find_tile_seq(const int32_t* cu, int B, int q, int s, int lane) {
-    return find_last(B, s, lane, [=](int b) { return cu[b] / q + b; });
+    // (unsigned: an entry far out of range finds some sequence, whose own entries are then checked)
+    return find_last(B, s, lane, [=](int b) { return (int)((uint32_t)(cu[b] / q) + (uint32_t)b); });
 }
 
 // The last sequence that begins at or before row i.
