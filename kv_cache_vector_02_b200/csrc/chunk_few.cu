@@ -74,6 +74,11 @@ struct FewSmem {
 };
 constexpr uint64_t kFWaitNs = 2000000000ull;
 constexpr float kFRescale = 8.f;  // log2 of what P may grow to before O is rescaled
+// ROWS = 32, where P carries the values' scalar v_t: a value below 2^-40 (a token's fp16 values, if
+// any is not 0, give 2^-29 at the least) counts as zero, and its P as if v_t were 2^-40.  That keeps
+// its weight in the sum: P is flushed below 2^-126, for such a token when its score is 86 - log2 v
+// below that of one of scalar v, a share of 2^-72 up to v = 2^14.
+constexpr float kFNoValue = 9.0949470177292824e-13f;
 constexpr uint32_t kFColS2 = 128, kFColO = 256, kFColP = 384;
 
 enum : int {
@@ -302,8 +307,7 @@ __global__ void __launch_bounds__(FewSmem<ROWS>::kThreads, 1)
                 scal[0] = r.state ? 0.f : r.kn * a.qscale;
                 if (PROD) scal[128] = r.state ? 0.f : r.kg * a.sscale;
                 if (M::kWeighted) {
-                    // (a zero value's 2^-100 keeps its weight in the sum and is 0 in P)
-                    const float v = fmaxf(fabsf(r.vn * a.vscale), 7.8886090522101181e-31f);
+                    const float v = fmaxf(fabsf(r.vn * a.vscale), kFNoValue);
                     const bool use = r.state == 0 && v < INFINITY;
                     scal[256] = use ? __log2f(v) : 0.f;
                     scal[384] = use ? __fdividef(1.f, v) : 0.f;
@@ -338,6 +342,11 @@ __global__ void __launch_bounds__(FewSmem<ROWS>::kThreads, 1)
                     if (!M::kWeighted) w[i] = *reinterpret_cast<const uint32_t*>(&x);
                 }
                 *reinterpret_cast<uint4*>(vt + ((uint32_t)((piece0 + c) ^ swap ^ (tok & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+            if (M::kWeighted && fabsf(r.vn * a.vscale) < kFNoValue) {
+#pragma unroll
+                for (int c = 0; c < kPer; ++c)
+                    *reinterpret_cast<uint4*>(vt + ((uint32_t)((piece0 + c) ^ swap ^ (tok & 7)) << 4)) = make_uint4(0u, 0u, 0u, 0u);
             }
             fence_proxy_async_shared();
             mbar_arrive_lead(lead, bar(kFBVFull + vb));

@@ -1,7 +1,10 @@
 """Edges of tq_chunk_attention and tq_prompt_attention: what test_gpu_chunk.py and
 test_gpu_prompt.py do not reach (bounds: attention64.py)."""
+import math
+
 import pytest
 
+from attention64 import U16
 from test_gpu_chunk import Case
 
 pytestmark = pytest.mark.gpu
@@ -14,6 +17,29 @@ WAYS = [(1, 4), (8, 4), (30, 4), (150, 4)]
 def _tq():
     from kv_cache_vector_02_b200 import tq
     return tq
+
+
+def _scalars(c):
+    """Views of a case's key norms, key gammas (None without a sketch) and value norms: [blocks, Hkv, 16]."""
+    import torch
+    k, v = c.kc.view(torch.float32), c.vc.view(torch.float32)
+    if c.c.key_mode == 0:
+        return k[..., -32:-16], k[..., -16:], v[..., -16:]
+    return k[..., -16:], None, v[..., -16:]
+
+
+def _refresh(c, orc):
+    """The case's 64-bit keys and values again, from its caches as they are now."""
+    import torch
+    o = orc.Oracle(128, c.c.bits, c.c.seed, rot=c.c.rotation, key_mode=c.c.key_mode)
+    kc, vc = c.kc.cpu().numpy(), c.vc.cpu().numpy()
+    kz = kc.copy()
+    if c.c.key_mode == 0:
+        kz[..., -64:] = 0
+    K, V, Kz = ([torch.as_tensor(o.decompress_paged(kind, cache, s, c.Hkv), device="cuda") for s in c.slots]
+                for kind, cache in ((0, kc), (1, vc), (0, kz)))
+    c.K, c.V = K, V
+    c.kerr, c.verr = [2 * U16 * x.norm(dim=2) for x in Kz], [2 * U16 * x.norm(dim=2) for x in V]
 
 
 @pytest.mark.parametrize("nq,G", WAYS)
@@ -41,3 +67,27 @@ def test_starts_and_lengths_far_out_of_range(orc, nq, G):
         out = c.run(seq_lens=torch.tensor([300, L], dtype=torch.int32, device="cuda"))
         assert tq.tq_get_device_error(c.c) == tq.DEVERR_SEQLEN
         assert torch.equal(out[:nq], ref[:nq]) and not bool(out[nq:].any())
+
+
+@pytest.mark.parametrize("nq,G", WAYS)
+def test_zero_values_count_in_the_softmax(orc, nq, G):
+    """Tokens whose values are 0 weigh as any: one token of large values, and thousands of zero
+    ones 13.5 (base 2) below its score that carry a quarter of the weight."""
+    c = Case(orc, [nq], [4096], G, 1, seed=20)
+    kn, kg, vn = _scalars(c)
+    page, r = int(c.slots[0][5]) // 16, 5
+    for x in (kn, kg, vn):
+        x.zero_()
+    kn[page, 0, r], vn[page, 0, r] = 4.0, 2.0 ** 13 * math.sqrt(128)
+    _refresh(c, orc)
+    key = c.K[0][5, 0]
+    c.q[:] = (key / key.norm() * 3).half()
+    scale = 13.5 * math.log(2.0) / float(c.q[0, 0].double() @ key)
+    c.check(c.run(scale=scale), "chunk zero values %d" % nq, scale=scale)
+    vn.zero_()
+    assert not bool(c.run(scale=scale).any())
+    # among ordinary ones
+    c = Case(orc, [nq], [700], G, 1, seed=21)
+    _scalars(c)[2][:, :, ::3] = 0.0
+    _refresh(c, orc)
+    c.check(c.run(), "chunk some zero values %d" % nq)
