@@ -452,6 +452,7 @@ ChunkPlan plan_chunk(const tq_ctx* ctx, int B, int total_q, int Hq, int Hkv, int
     };
     if (p.few) {
         p.k_off = take((size_t)total_q * Hq * 2 * kDim * 2);  // the rotated queries
+        p.v_off = take((size_t)total_q * Hq * 4);             // and their factors
         p.part_off = take((size_t)p.splits * total_q * Hq * kDim * 4);
         p.ml_off = take((size_t)p.splits * total_q * Hq * 8);
         p.bytes = off + 256;

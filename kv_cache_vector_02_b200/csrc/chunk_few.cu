@@ -6,7 +6,8 @@
 //         a_t = scale n_t / sqrt(d),  b_t = scale gamma_t sqrt(pi/2) / d,
 //   acc = sum_t p_t (n_t / sqrt(d)) c_v,   o = R acc / sum_t p_t.
 //
-// few_rotate_kernel   q' and s of every (query, head), fp16 (R^T as fp16 hi + lo)
+// few_rotate_kernel   q' and s of every (query, head), fp16 (R^T as fp16 hi + lo), with a factor
+//                     for the rows that would pass fp16
 // few_attend_kernel   one CTA per (32 or 128 rows, kv head, split of the tokens); a row is a
 //                     (query, query head of the group) pair.  Per tile of 128 tokens:
 //   coding warps   two threads per token (32 rows: 16 warps, four per token) turn its packed
@@ -109,6 +110,7 @@ struct FewArgs {
     LevelTable tk, tv;
     float qscale, sscale;    // scale log2(e) / sqrt(d) (times the key levels' scale), scale log2(e) sqrt(pi/2) / d
     float vscale;            // 1 / sqrt(d) times the value levels' scale
+    const float* qfactor;    // [total_q * Hq] what q' and s of the row are to be multiplied by (a power of two)
     float* part;             // [splits][total_q * Hq][128] unscaled sums, rotated
     float2* ml;              // [splits][total_q * Hq] maximum (base 2) and sum
     void* out;               // rows of sequences with impossible lengths are zeroed here
@@ -443,6 +445,11 @@ __global__ void __launch_bounds__(FewSmem<ROWS>::kThreads, 1)
         const int limit = live ? off + q0 + row / a.G - j0 * kFN : -1;  // its last token, from the split's first
         const int masked_from = (off + q0 + 1) / kFN - j0;             // first tile with a masked pair
         float* tops = reinterpret_cast<float*>(smem + M::kOffTop) + lane;  // [kParts][32]
+        // D1 and D2 are 1 / fac of the row's products.  With 32 rows the scores of a warp that has
+        // such a row are put right as they come; with 128 the exponent's argument takes the factor.
+        const float fac = live ? a.qfactor[out_row(row)] : 1.f;
+        const float rest = M::kWeighted ? 1.f : fac;
+        const bool scaled = __any_sync(0xffffffffu, fac != 1.f) != 0;
         float m = -INFINITY;
         float2 sum[2] = {{0.f, 0.f}, {0.f, 0.f}};
         bool ok = true;
@@ -487,6 +494,18 @@ __global__ void __launch_bounds__(FewSmem<ROWS>::kThreads, 1)
                     x[3] = __float_as_uint(v.y);
                 }
             }
+            if (M::kWeighted && scaled) {  // (seldom)
+                // a rounding of log2 v_t is multiplied too: 2^-24 |log2 v_t| fac, at most 2^-15 |log2 v_t|
+#pragma unroll
+                for (int q = 0; q < kCols / 4; ++q) {
+                    const float4 fl = sc[64 + q];
+                    uint32_t* x = &s[q / 8][4 * (q % 8)];
+                    x[0] = __float_as_uint(fmaf(__uint_as_float(x[0]) - fl.x, fac, fl.x));
+                    x[1] = __float_as_uint(fmaf(__uint_as_float(x[1]) - fl.y, fac, fl.y));
+                    x[2] = __float_as_uint(fmaf(__uint_as_float(x[2]) - fl.z, fac, fl.z));
+                    x[3] = __float_as_uint(fmaf(__uint_as_float(x[3]) - fl.w, fac, fl.w));
+                }
+            }
             const uint2 pb = *reinterpret_cast<const uint2*>(page_bad + 8 * (j & 1));
             tc_fence_before();
             mbar_arrive_lead(lead, bar(kFBL));
@@ -521,6 +540,7 @@ __global__ void __launch_bounds__(FewSmem<ROWS>::kThreads, 1)
                 }
                 top = few_max3(top, few_max3(m0, m0, __uint_as_float(s[q][15])), few_max3(m1, m1, __uint_as_float(s[q][31])));
             }
+            if (!M::kWeighted) top *= rest;
             // a NaN or infinite score makes the row's sum and outputs NaN; the maximum carries it
             if (!(top < INFINITY)) top = NAN;
             auto grows = [&](float t) { return t > m + kFRescale || (m == -INFINITY && t > m) || (t != t && m == m); };
@@ -568,7 +588,7 @@ __global__ void __launch_bounds__(FewSmem<ROWS>::kThreads, 1)
                 for (int e = 0; e < 8; ++e) {
                     const int i = 16 * q + 2 * e;
                     float2 x = make_float2(__uint_as_float(s[i / 32][i % 32]), __uint_as_float(s[i / 32][i % 32 + 1]));
-                    x = __fadd2_rn(x, nm);
+                    x = M::kWeighted ? __fadd2_rn(x, nm) : __ffma2_rn(x, make_float2(rest, rest), nm);
                     x.x = few_ex2(x.x);
                     x.y = few_ex2(x.y);
                     if (M::kWeighted) {  // the weight in the sum is without the value's scalar
@@ -633,6 +653,10 @@ __global__ void __launch_bounds__(FewSmem<ROWS>::kThreads, 1)
 // q' = R^T q and s = S q of 64 rows and 32 output coordinates per CTA, 16 rows per warp, on
 // mma.sync (m16n8k16); R^T as fp16 hi + lo, fp32 sums, rounded once.  The matrices' 16-byte
 // pieces lie at k ^ (row % 8).
+//
+// No coordinate of q' or s is larger than 128 times the query's largest (S has entries +-1), which
+// passes fp16 from 512 on.  Rows whose bound passes 61440 are stored times a power of two that
+// brings it into 2^14 .. 2^15, and the attention multiplies their products by its inverse, `factor`.
 constexpr int kRotThreads = 128, kRotRows = 64, kRotCols = 32;
 constexpr uint32_t kRotMat = kRotCols * kDim * 2;
 
@@ -640,9 +664,23 @@ __device__ __forceinline__ uint32_t rot_word(const uint8_t* m, int r, int w) {
     return *reinterpret_cast<const uint32_t*>(m + r * 256 + ((((w >> 2) ^ (r & 7)) << 4) | ((w & 3) << 2)));
 }
 
+// The row's factor, 1 if its bound fits (or the row is not finite): the four lanes of a row's group
+// hold its coordinates between them.
+__device__ __forceinline__ float rot_factor(const uint32_t (&qa)[8][4], int first) {
+    __half2 m = __float2half2_rn(0.f);
+#pragma unroll
+    for (int ks = 0; ks < 8; ++ks)
+#pragma unroll
+        for (int i = first; i < 4; i += 2) m = __hmax2(m, __habs2(*reinterpret_cast<const __half2*>(&qa[ks][i])));
+    float most = (float)kDim * __half2float(__hmax(__low2half(m), __high2half(m)));
+    most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 1));
+    most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 2));
+    return most > 61440.f && most < INFINITY ? scalbnf(1.f, ilogbf(most) - 14) : 1.f;
+}
+
 __global__ void __launch_bounds__(kRotThreads) few_rotate_kernel(const uint16_t* q, long long rows, const uint16_t* RTh,
                                                                  const uint16_t* RTl, const uint16_t* Sh, int prod,
-                                                                 uint16_t* out) {
+                                                                 uint16_t* out, float* factor) {
     __shared__ __align__(16) uint8_t smem[3 * kRotMat];
     const uint32_t base = smem_u32(smem);
     const uint16_t* src[3] = {RTh, RTl, Sh};
@@ -668,6 +706,12 @@ __global__ void __launch_bounds__(kRotThreads) few_rotate_kernel(const uint16_t*
         qa[ks][2] = r0 ? q0[8 * ks + c + 4] : 0u;
         qa[ks][3] = r1 ? q1[8 * ks + c + 4] : 0u;
     }
+    const float f0 = rot_factor(qa, 0), f1 = rot_factor(qa, 1);
+    if (blockIdx.y == 0 && c == 0) {
+        if (r0) factor[i0] = f0;
+        if (r1) factor[i1] = f1;
+    }
+    const float u0 = 1.f / f0, u1 = 1.f / f1;
     cp_async_wait<0>();
     __syncthreads();
 #pragma unroll 1
@@ -687,12 +731,12 @@ __global__ void __launch_bounds__(kRotThreads) few_rotate_kernel(const uint16_t*
         uint32_t* o0 = reinterpret_cast<uint32_t*>(out + i0 * 2 * kDim + n0) + 4 * nt + c;
         uint32_t* o1 = reinterpret_cast<uint32_t*>(out + i1 * 2 * kDim + n0) + 4 * nt + c;
         if (r0) {
-            o0[0] = f2h2(dq[0], dq[1]);
-            if (prod) o0[kDim / 2] = f2h2(ds[0], ds[1]);
+            o0[0] = f2h2(dq[0] * u0, dq[1] * u0);
+            if (prod) o0[kDim / 2] = f2h2(ds[0] * u0, ds[1] * u0);
         }
         if (r1) {
-            o1[0] = f2h2(dq[2], dq[3]);
-            if (prod) o1[kDim / 2] = f2h2(ds[2], ds[3]);
+            o1[0] = f2h2(dq[2] * u1, dq[3] * u1);
+            if (prod) o1[kDim / 2] = f2h2(ds[2] * u1, ds[3] * u1);
         }
     }
 }
@@ -855,10 +899,11 @@ cudaError_t launch_chunk_few(const tq_ctx* ctx, const ChunkPlan& plan, const Chu
     const long long rows = (long long)c.total_q * c.Hq;
     const bool prod = ctx->lay_key.prod;
     uint16_t* rot = reinterpret_cast<uint16_t*>(ws + plan.k_off);
+    float* factor = reinterpret_cast<float*>(ws + plan.v_off);
     const long long rot_blocks = (rows + kRotRows - 1) / kRotRows;
     if (rot_blocks > 0x7FFFFFFFll) return cudaErrorInvalidValue;
     cudaError_t e = launch_after(few_rotate_kernel, dim3((unsigned)rot_blocks, kDim / kRotCols), kRotThreads, 0, stream, c.q,
-                                 rows, ctx->dev.RTh, ctx->dev.RTl, ctx->dev.Sh, prod ? 1 : 0, rot);
+                                 rows, ctx->dev.RTh, ctx->dev.RTl, ctx->dev.Sh, prod ? 1 : 0, rot, factor);
     if (e != cudaSuccess) return e;
 
     FewArgs a{};
@@ -884,6 +929,7 @@ cudaError_t launch_chunk_few(const tq_ctx* ctx, const ChunkPlan& plan, const Chu
     a.vscale = a.tv.scale / std::sqrt((float)kDim);
     a.qscale = scale_log2 * a.tk.scale / std::sqrt((float)kDim);
     a.sscale = scale_log2 * 1.2533141373155003f / (float)kDim;
+    a.qfactor = factor;
     a.part = reinterpret_cast<float*>(ws + plan.part_off);
     a.ml = reinterpret_cast<float2*>(ws + plan.ml_off);
     a.out = c.out;

@@ -209,7 +209,7 @@ struct ChunkPlan {
     int kv_pad;          // tokens of a sequence, rounded up to whole tiles of 128
     int heads;           // kv heads decompressed at a time
     int splits;          // of the tokens, in the attention
-    size_t k_off, v_off; // workspace offsets (bytes): fp16 [B * kv_pad][heads][128] (few: k_off, rotated queries)
+    size_t k_off, v_off; // workspace offsets (bytes): fp16 [B * kv_pad][heads][128] (few: rotated queries, their factors)
     size_t pages_off;    // u8 [B][kv_pad / 128]
     size_t part_off, ml_off;
     size_t bytes;

@@ -91,3 +91,33 @@ def test_zero_values_count_in_the_softmax(orc, nq, G):
     _scalars(c)[2][:, :, ::3] = 0.0
     _refresh(c, orc)
     c.check(c.run(), "chunk some zero values %d" % nq)
+
+
+@pytest.mark.parametrize("nq,G", WAYS)
+@pytest.mark.parametrize("rot,km", [(0, 0), (1, 0), (1, 1)])
+def test_queries_of_any_fp16_size(orc, nq, G, rot, km):
+    """Queries whose rotation or sketch lies beyond fp16: along a row of the sketch matrix and a
+    column of the rotation, beside ordinary and tiny ones."""
+    import torch
+    tq = _tq()
+    c = Case(orc, [nq, 3], [400, 90], G, 1, rot=rot, km=km, seed=23)
+    P = tq.tq_export_params(c.c)
+    S, R = torch.as_tensor(P["S"], device="cuda").double(), torch.as_tensor(P["R"], device="cuda").double()
+    loud = [S[3] * 500, S[7] * 60000, -S[9] * 2000, R[:, 5] * (60000 / R[:, 5].abs().max()), R[:, 0] * 5e4]
+    for i in range(min(nq * G, 40)):
+        if i % 6 < 5:
+            c.q[i // G, i % G] = loud[i % 6].half()
+        else:
+            c.q[i // G, i % G] *= 2.0 ** -8
+    assert bool(torch.isfinite(c.q).all())
+    # (scores of the loudest: 60000 sqrt(128) * |k| / sqrt(128) at random angles, times the scale)
+    scale = 2e-6
+    out = c.run(scale=scale)
+    assert bool(torch.isfinite(out).all())
+    c.check(out, "chunk loud queries %d" % nq, scale=scale)
+    # a query that is not finite reaches its own head's row only
+    c.q[0, 1] = float("inf")
+    bad = c.run(scale=scale)
+    keep = torch.ones(bad.shape[:2], dtype=torch.bool, device="cuda")
+    keep[0, 1] = False
+    assert torch.equal(bad[keep], out[keep]) and bool(torch.isnan(bad[0, 1]).all())
