@@ -124,11 +124,12 @@ def _current_device() -> int | None:
 class Context:
     """Owns one libtq context (tq_init / tq_destroy)."""
 
-    def __init__(self, handle: int, head_dim: int, bits: int, seed: int, rotation: int, key_mode: int):
+    def __init__(self, handle: int, head_dim: int, bits: int, seed: int, rotation: int, key_mode: int,
+                 host_only: bool = False):
         self.handle = handle
         self.head_dim, self.bits, self.seed, self.rotation, self.key_mode = head_dim, bits, seed, rotation, key_mode
         self._chunk = {}  # chunk bytes by kind, asked of the library once
-        self.device = _current_device()  # what tq_init bound the context to
+        self.device = None if host_only else _current_device()  # what tq_init bound the context to
 
     def __del__(self):
         h = getattr(self, "handle", None)
@@ -153,7 +154,7 @@ def tq_init_ex(head_dim: int = 128, bits: int = 4, seed: int = 0, rotation: int 
     """tq_init with TQ_FLAG_* options (see tq.h)."""
     h = ctypes.c_void_p()
     _check(_lib.tq_init_ex(head_dim, bits, seed, rotation, key_mode, flags, ctypes.byref(h)), "tq_init_ex")
-    return Context(h.value, head_dim, bits, seed, rotation, key_mode)
+    return Context(h.value, head_dim, bits, seed, rotation, key_mode, bool(flags & FLAG_HOST_ONLY))
 
 
 def tq_init_host(head_dim: int = 128, bits: int = 4, seed: int = 0, rotation: int = ROT_HAAR,
@@ -161,7 +162,7 @@ def tq_init_host(head_dim: int = 128, bits: int = 4, seed: int = 0, rotation: in
     """Host-only context (parameters on the host, no device touched)."""
     h = ctypes.c_void_p()
     _check(_lib.tq_init_host(head_dim, bits, seed, rotation, key_mode, ctypes.byref(h)), "tq_init_host")
-    return Context(h.value, head_dim, bits, seed, rotation, key_mode)
+    return Context(h.value, head_dim, bits, seed, rotation, key_mode, True)
 
 
 def tq_destroy(ctx: Context):
