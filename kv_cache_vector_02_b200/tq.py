@@ -338,9 +338,9 @@ def _same_device(what: str, first, *others) -> int:
 
 
 def _check_device(ctx: Context, what: str, dev: int):
-    if ctx.device is not None and dev >= 0 and dev != ctx.device:
-        raise TQError(TQ_ERR_INVALID_ARG, "%s: tensors on cuda:%d must be on the context's device, cuda:%d" % (
-            what, dev, ctx.device))
+    if ctx.device is not None and dev != ctx.device:
+        raise TQError(TQ_ERR_INVALID_ARG, "%s: tensors on %s must be on the context's device, cuda:%d" % (
+            what, "cuda:%d" % dev if dev >= 0 else "the host", ctx.device))
 
 
 def _stream_on(stream, dev: int) -> int:
@@ -389,6 +389,8 @@ def tq_rope(table: RopeTable, q, k, positions, q_out=None, k_out=None, transpose
         raise TQError(TQ_ERR_INVALID_ARG, "%s: k_out without k" % what)
     _expect(positions, (T,), (torch.int32,), what, "positions")
     dev = _same_device(what, ref, k, q_out, k_out, positions)
+    if dev < 0 and T > 0:
+        raise TQError(TQ_ERR_INVALID_ARG, "%s: tensors on %s must be on a CUDA device" % (what, ref.device))
     call = (table, _ptr(q), sq, _ptr(k), sk, T, Hq, Hkv, positions.data_ptr(), _ptr(q_out), sqo, _ptr(k_out), sko,
             1 if transpose else 0, _stream_on(stream, dev))
     if dev >= 0 and dev != torch.cuda.current_device():
