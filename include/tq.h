@@ -392,7 +392,8 @@ TQ_API size_t tq_chunk_workspace_bytes(const tq_ctx* ctx, int B, int total_q, in
  *   max_seq_len    : host-side upper bound of seq_lens.
  *   scale          : softmax scale; 0 for the default 1/sqrt(d).
  *   out_dev        : [total_q][Hq][128], fp16 (out_fp32 = 0) or fp32 (out_fp32 = 1); rows in
- *                    no sequence are left as they were.  Must not overlap q or the workspace.
+ *                    no sequence are left as they were.  Neither it nor the workspace may overlap
+ *                    the other, q, a cache or a list (TQ_ERR_INVALID_ARG).
  *   workspace_dev  : >= tq_chunk_workspace_bytes(...) bytes, 16-byte aligned.
  * A cache row behind a sequence's last token may hold anything, and a token's norms that are
  * not finite reach the queries that attend it only (for value norms up to 2^14 sqrt(d), beyond

@@ -606,8 +606,16 @@ tq_status tq_chunk_attention(const tq_ctx* ctx, const uint16_t* q, const int32_t
     if (plan.bytes == 0 || workspace_bytes < plan.bytes) return TQ_ERR_INVALID_ARG;
     const long long out_bytes = (long long)total_q * Hq * kDim * (out_fp32 ? 4 : 2);
     const Rows o{out, 1, out_bytes, out_bytes}, w{workspace, 1, (long long)plan.bytes, (long long)plan.bytes};
-    const Rows qr = fp16_rows(q, total_q, Hq, (int64_t)Hq * kDim);
-    if (overlap(o, qr) || overlap(o, w) || overlap(w, qr)) return TQ_ERR_INVALID_ARG;
+    auto whole = [](const void* p, long long bytes) { return Rows{p, bytes > 0, bytes, bytes}; };
+    const Rows reads[] = {fp16_rows(q, total_q, Hq, (int64_t)Hq * kDim),
+                          whole(cu_q, ((long long)B + 1) * 4),
+                          whole(seq_lens, (long long)B * 4),
+                          whole(block_table, (long long)B * max_blocks * 4),
+                          whole(k_cache, (long long)num_blocks * Hkv * ctx->lay_key.bytes),
+                          whole(v_cache, (long long)num_blocks * Hkv * ctx->lay_value.bytes)};
+    if (overlap(o, w)) return TQ_ERR_INVALID_ARG;
+    for (const Rows& r : reads)
+        if (overlap(o, r) || overlap(w, r)) return TQ_ERR_INVALID_ARG;
     if (scale == 0.f) scale = 1.0f / std::sqrt(float(kDim));
     DeviceGuard dev(ctx->device);
     if (!dev.ok) return TQ_ERR_CUDA;

@@ -121,3 +121,39 @@ def test_queries_of_any_fp16_size(orc, nq, G, rot, km):
     keep = torch.ones(bad.shape[:2], dtype=torch.bool, device="cuda")
     keep[0, 1] = False
     assert torch.equal(bad[keep], out[keep]) and bool(torch.isnan(bad[0, 1]).all())
+
+
+@pytest.mark.parametrize("nq,G", WAYS)
+def test_outputs_and_workspaces_over_inputs(orc, nq, G):
+    """An output or a workspace over a list or a cache is refused, and the input stays as it was."""
+    import torch
+    tq = _tq()
+    c = Case(orc, [nq], [300], G, 1, seed=24)
+    need = tq.tq_chunk_workspace_bytes(c.c, 1, nq, G, 1, 300)
+    room = torch.zeros(need + (1 << 20), dtype=torch.uint8, device="cuda")
+    out = torch.empty(c.q.shape, dtype=torch.float32, device="cuda")
+
+    def inside(t, at):
+        """A copy of t in `room`, `at` bytes from its start."""
+        n = t.numel() * t.element_size()
+        view = room[at:at + n].view(t.dtype).view(t.shape)
+        view.copy_(t)
+        return view
+
+    n_out = out.numel() * 4
+    for name in ("cu_q", "seq_lens", "block_table", "k_cache", "v_cache"):
+        t = dict(cu_q=c.cu, seq_lens=c.L, block_table=c.bt, k_cache=c.kc, v_cache=c.vc)[name]
+        for at, kw in ((0, dict(ws=room[:need])), (need - 16, dict(ws=room[:need])),
+                       (0, dict(out=room[:n_out].view(torch.float32).view(out.shape))),
+                       (n_out - 16, dict(out=room[:n_out].view(torch.float32).view(out.shape)))):
+            view = inside(t, at)
+            n0 = tq.tq_launch_count()
+            with pytest.raises(tq.TQError) as e:
+                c.run(**{name: view}, **kw)
+            assert e.value.status == tq.TQ_ERR_INVALID_ARG and tq.tq_launch_count() == n0, (name, at)
+            assert torch.equal(view, t)
+        # right behind a workspace and an output: allowed
+        behind = -(-max(need, n_out) // 256) * 256
+        c.check(c.run(ws=room[:need], **{name: inside(t, behind)}), "chunk %s behind the workspace" % name)
+        o = room[:n_out].view(torch.float32).view(out.shape)
+        c.check(c.run(out=o, **{name: inside(t, behind)}), "chunk %s behind the output" % name)
