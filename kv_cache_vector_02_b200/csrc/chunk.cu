@@ -417,7 +417,8 @@ ChunkPlan plan_chunk(const tq_ctx* ctx, int B, int total_q, int Hq, int Hkv, int
     p.few = (long long)total_q * (Hq / Hkv) <= (long long)kFewRows * B;
     const long long tiles = max_seq_len > 0 ? ((long long)max_seq_len + 127) / 128 : 1;
     const long long rows = (long long)B * tiles * 128;
-    if (rows > 0x7FFFFFFFll) return p;  // TMA coordinates are 32-bit
+    // TMA coordinates and token numbers are 32-bit; chunk_few.cu counts up to five tiles past the last
+    if (rows > 0x7FFFFFFFll - 1024) return p;
     p.kv_pad = (int)(tiles * 128);
     const size_t head_bytes = (size_t)rows * kDim * 2 * 2;
     p.heads = Hkv;

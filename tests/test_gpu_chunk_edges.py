@@ -5,6 +5,7 @@ import math
 import pytest
 
 from attention64 import U16
+from parity import gpu_ctx
 from test_gpu_chunk import Case
 
 pytestmark = pytest.mark.gpu
@@ -157,3 +158,12 @@ def test_outputs_and_workspaces_over_inputs(orc, nq, G):
         c.check(c.run(ws=room[:need], **{name: inside(t, behind)}), "chunk %s behind the workspace" % name)
         o = room[:n_out].view(torch.float32).view(out.shape)
         c.check(c.run(out=o, **{name: inside(t, behind)}), "chunk %s behind the output" % name)
+
+
+def test_lengths_next_to_31_bits():
+    """Token numbers a few tiles past the longest sequence stay within 32 bits."""
+    tq = _tq()
+    c = gpu_ctx()
+    for top in (2 ** 31 - 1, 2 ** 31 - 200, 2 ** 31 - 1024):
+        assert tq._lib.tq_chunk_workspace_bytes(c.handle, 1, 1, 1, 1, top) == 0, top
+    assert tq._lib.tq_chunk_workspace_bytes(c.handle, 1, 1, 1, 1, 2 ** 31 - 4096) > 0
