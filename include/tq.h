@@ -366,8 +366,14 @@ TQ_API tq_status tq_prompt_attention(const tq_ctx* ctx, const uint16_t* q_dev, i
 /*
  * tq_chunk_workspace_bytes -- device scratch needed by tq_chunk_attention for B sequences,
  * total_q queries in all, Hq query heads over Hkv kv heads and at most max_seq_len cached
- * tokens a sequence (0 on invalid arguments).  Any contents; nothing in it outlives a call.
- * Two calls that run at the same time need separate workspaces.
+ * tokens a sequence (0 on invalid arguments, and where B sequences of max_seq_len tokens,
+ * rounded up to 128, pass 2^31 - 1024 tokens).  It follows these bounds, not the lengths in
+ * use.  Any contents; nothing in it outlives a call.  Two calls that run at the same time
+ * need separate workspaces.
+ * It is enough for every call with the same B and heads and no larger total_q or
+ * max_seq_len (a batch may be filled up with empty sequences).  Such a call can ask for more
+ * than a larger one: it then splits its tokens over fewer CTAs, or decompresses fewer heads
+ * at a time, than with a workspace of its own size, and its sums' order follows.
  */
 TQ_API size_t tq_chunk_workspace_bytes(const tq_ctx* ctx, int B, int total_q, int Hq, int Hkv, int max_seq_len);
 
@@ -394,12 +400,14 @@ TQ_API size_t tq_chunk_workspace_bytes(const tq_ctx* ctx, int B, int total_q, in
  *   out_dev        : [total_q][Hq][128], fp16 (out_fp32 = 0) or fp32 (out_fp32 = 1); rows in
  *                    no sequence are left as they were.  Neither it nor the workspace may overlap
  *                    the other, q, a cache or a list (TQ_ERR_INVALID_ARG).
- *   workspace_dev  : >= tq_chunk_workspace_bytes(...) bytes, 16-byte aligned.
+ *   workspace_dev  : >= tq_chunk_workspace_bytes(...) bytes, 16-byte aligned; for this call or
+ *                    for a larger one (see there).
  * A cache row behind a sequence's last token may hold anything, and a token's norms that are
  * not finite reach the queries that attend it only (for value norms up to 2^14 sqrt(d), beyond
  * which its values overflow fp16).  Three launches, or with many queries two or three for as
- * many kv heads as fit 1 GiB of decompressed tokens at a time, queued on stream, on the
- * context's device; total_q = 0 or B = 0 launches nothing.
+ * many kv heads at a time as fit 1 GiB of decompressed tokens (one head at the least: 512
+ * bytes a token of B sequences of max_seq_len), queued on stream, on the context's device;
+ * total_q = 0 or B = 0 launches nothing.
  */
 TQ_API tq_status tq_chunk_attention(const tq_ctx* ctx, const uint16_t* q_dev, const int32_t* cu_q_dev,
                                     const uint8_t* k_cache_dev, const uint8_t* v_cache_dev, int num_blocks,

@@ -28,6 +28,7 @@
 // lookups, MMAs and stores take turns on one set of operand tiles.  It is 12 us of the 131 above
 // and 188 of the 1310; the rest is the attention's.
 #include <cmath>
+#include <cstdint>
 
 #include <cuda.h>
 
@@ -53,7 +54,8 @@ static_assert(kUSmem <= 232448, "shared memory budget");
 constexpr uint64_t kUWaitNs = 2000000000ull;
 // At most so many (query, head of a group) rows a sequence on average: chunk_few.cu.
 constexpr int kFewRows = 128;
-constexpr size_t kDecompressedMost = size_t(1) << 30;   // keys and values decompressed at a time
+// Keys and values decompressed at a time: as many kv heads as fit, one at the least.
+constexpr size_t kDecompressedMost = size_t(1) << 30;
 
 enum : int { kUBConst = 0, kUBA = 1, kUBD = 2, kUBDEmpty = 3, kUNumBars = 4 };
 
@@ -412,7 +414,16 @@ size_t up256(size_t x) { return (x + 255) & ~size_t(255); }
 
 }  // namespace
 
-ChunkPlan plan_chunk(const tq_ctx* ctx, int B, int total_q, int Hq, int Hkv, int max_seq_len) {
+// Workspace of the splits' partial results; of the few-row way.
+static size_t part_bytes(int splits, int total_q, int Hq) {
+    const size_t rows = (size_t)splits * total_q * Hq;
+    return up256(rows * kDim * 4) + up256(rows * 8);
+}
+static size_t few_bytes(int splits, int total_q, int Hq) {
+    return up256((size_t)total_q * Hq * 2 * kDim * 2) + up256((size_t)total_q * Hq * 4) + part_bytes(splits, total_q, Hq) + 256;
+}
+
+ChunkPlan plan_chunk(const tq_ctx* ctx, int B, int total_q, int Hq, int Hkv, int max_seq_len, size_t limit) {
     ChunkPlan p{};
     p.few = (long long)total_q * (Hq / Hkv) <= (long long)kFewRows * B;
     const long long tiles = max_seq_len > 0 ? ((long long)max_seq_len + 127) / 128 : 1;
@@ -421,13 +432,23 @@ ChunkPlan plan_chunk(const tq_ctx* ctx, int B, int total_q, int Hq, int Hkv, int
     if (rows > 0x7FFFFFFFll - 1024) return p;
     p.kv_pad = (int)(tiles * 128);
     const size_t head_bytes = (size_t)rows * kDim * 2 * 2;
+    const size_t fixed = up256((size_t)B * tiles) + 256;  // (many rows: besides tokens and partial results)
     p.heads = Hkv;
-    if (!p.few && head_bytes * Hkv > kDecompressedMost) {
-        p.heads = (int)(kDecompressedMost / (head_bytes ? head_bytes : 1));
-        if (p.heads < 1) p.heads = 1;
+    if (!p.few) {
+        size_t room = head_bytes > kDecompressedMost ? head_bytes : kDecompressedMost;
+        const size_t left = limit > fixed ? limit - fixed : 0;
+        if (room > left) room = left;
+        if (head_bytes * Hkv > room) p.heads = (int)(room / head_bytes);
+        if (p.heads < 1) return p;
     }
+    auto bytes = [&](int splits) {
+        if (p.few) return few_bytes(splits, total_q, Hq);
+        return head_bytes * p.heads + fixed + (splits > 1 ? part_bytes(splits, total_q, Hq) : 0);
+    };
+    if (bytes(1) > limit) return p;
     // Splits of the tokens: as many as make the waves over the SMs shortest, each split
-    // costing about three tiles more (its start and end, and its part of the join).
+    // costing about three tiles more (its start and end, and its part of the join); of those
+    // that the workspace has room for.
     const int G = Hq / Hkv;
     // rows per CTA: 32 where a sequence has no more on average (chunk_few.cu has more buffers then)
     p.rows = !p.few ? 256 : G <= 32 && (long long)total_q * G <= 32ll * B ? 32 : 128;
@@ -437,7 +458,7 @@ ChunkPlan plan_chunk(const tq_ctx* ctx, int B, int total_q, int Hq, int Hkv, int
     ctas *= p.heads;
     p.splits = 1;
     double best = 0.;
-    for (int s = 1; s <= 32 && (s == 1 || tiles >= (p.few ? 2 : 4) * s); ++s) {
+    for (int s = 1; s <= 32 && (s == 1 || tiles >= (p.few ? 2 : 4) * s) && bytes(s) <= limit; ++s) {
         const double waves = double((ctas * s + ctx->sm_count - 1) / ctx->sm_count);
         const double cost = waves * (double(tiles) / s + 3.) + (s > 1 ? 2. : 0.);
         if (s == 1 || cost < best) {
@@ -454,20 +475,29 @@ ChunkPlan plan_chunk(const tq_ctx* ctx, int B, int total_q, int Hq, int Hkv, int
     if (p.few) {
         p.k_off = take((size_t)total_q * Hq * 2 * kDim * 2);  // the rotated queries
         p.v_off = take((size_t)total_q * Hq * 4);             // and their factors
-        p.part_off = take((size_t)p.splits * total_q * Hq * kDim * 4);
-        p.ml_off = take((size_t)p.splits * total_q * Hq * 8);
-        p.bytes = off + 256;
-        return p;
+    } else {
+        p.k_off = take(head_bytes / 2 * p.heads);
+        p.v_off = take(head_bytes / 2 * p.heads);
+        p.pages_off = take((size_t)B * tiles);
     }
-    p.k_off = take(head_bytes / 2 * p.heads);
-    p.v_off = take(head_bytes / 2 * p.heads);
-    p.pages_off = take((size_t)B * tiles);
-    if (p.splits > 1) {
+    if (p.few || p.splits > 1) {
         p.part_off = take((size_t)p.splits * total_q * Hq * kDim * 4);
         p.ml_off = take((size_t)p.splits * total_q * Hq * 8);
     }
-    p.bytes = off + 256;
+    p.bytes = bytes(p.splits);
     return p;
+}
+
+// A call of as many sequences with fewer queries or tokens might choose more splits, more heads a
+// pass or the other way.  It does with fewer splits and heads where it has to (plan_chunk), and
+// then needs no more than this call, but for the few-row way's queries: the most of them are
+// counted here.
+size_t chunk_workspace(const tq_ctx* ctx, int B, int total_q, int Hq, int Hkv, int max_seq_len) {
+    const ChunkPlan p = plan_chunk(ctx, B, total_q, Hq, Hkv, max_seq_len, SIZE_MAX);
+    if (p.bytes == 0 || p.few) return p.bytes;
+    const long long most = (long long)kFewRows * B / (Hq / Hkv);
+    const size_t few = few_bytes(1, (int)(most < total_q ? most : total_q), Hq);
+    return few > p.bytes ? few : p.bytes;
 }
 
 cudaError_t launch_chunk(const tq_ctx* ctx, const ChunkPlan& plan, const ChunkCall& c, cudaStream_t stream) {

@@ -583,7 +583,7 @@ tq_status tq_prompt_attention(const tq_ctx* ctx, const uint16_t* q, int64_t q_st
 size_t tq_chunk_workspace_bytes(const tq_ctx* ctx, int B, int total_q, int Hq, int Hkv, int max_seq_len) {
     if (!ctx || ctx->host_only || B < 1 || total_q < 0 || Hq < 1 || Hkv < 1 || max_seq_len < 0) return 0;
     if (Hq % Hkv != 0 || Hq / Hkv > 128) return 0;
-    return tq::plan_chunk(ctx, B, total_q, Hq, Hkv, max_seq_len).bytes;
+    return tq::chunk_workspace(ctx, B, total_q, Hq, Hkv, max_seq_len);
 }
 
 tq_status tq_chunk_attention(const tq_ctx* ctx, const uint16_t* q, const int32_t* cu_q, const uint8_t* k_cache,
@@ -602,8 +602,8 @@ tq_status tq_chunk_attention(const tq_ctx* ctx, const uint16_t* q, const int32_t
         return TQ_ERR_INVALID_ARG;
     if (!aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(out) || !aligned16(workspace))
         return TQ_ERR_INVALID_ARG;
-    const tq::ChunkPlan plan = tq::plan_chunk(ctx, B, total_q, Hq, Hkv, max_seq_len);
-    if (plan.bytes == 0 || workspace_bytes < plan.bytes) return TQ_ERR_INVALID_ARG;
+    const tq::ChunkPlan plan = tq::plan_chunk(ctx, B, total_q, Hq, Hkv, max_seq_len, workspace_bytes);
+    if (plan.bytes == 0) return TQ_ERR_INVALID_ARG;
     const long long out_bytes = (long long)total_q * Hq * kDim * (out_fp32 ? 4 : 2);
     const Rows o{out, 1, out_bytes, out_bytes}, w{workspace, 1, (long long)plan.bytes, (long long)plan.bytes};
     auto whole = [](const void* p, long long bytes) { return Rows{p, bytes > 0, bytes, bytes}; };

@@ -214,7 +214,10 @@ struct ChunkPlan {
     size_t part_off, ml_off;
     size_t bytes;
 };
-ChunkPlan plan_chunk(const tq_ctx* ctx, int B, int total_q, int Hq, int Hkv, int max_seq_len);
+// bytes = 0: no plan fits `limit` bytes of workspace (or 32-bit token numbers).
+ChunkPlan plan_chunk(const tq_ctx* ctx, int B, int total_q, int Hq, int Hkv, int max_seq_len, size_t limit);
+// Workspace of the best plan, enough for some plan of every call with fewer queries or tokens.
+size_t chunk_workspace(const tq_ctx* ctx, int B, int total_q, int Hq, int Hkv, int max_seq_len);
 struct ChunkCall {
     const uint16_t* q;        // [total_q][Hq][128]
     const int32_t* cu_q;      // [B + 1]

@@ -2,6 +2,7 @@
 test_gpu_prompt.py do not reach (bounds: attention64.py)."""
 import math
 
+import numpy as np
 import pytest
 
 from attention64 import U16
@@ -167,3 +168,34 @@ def test_lengths_next_to_31_bits():
     for top in (2 ** 31 - 1, 2 ** 31 - 200, 2 ** 31 - 1024):
         assert tq._lib.tq_chunk_workspace_bytes(c.handle, 1, 1, 1, 1, top) == 0, top
     assert tq._lib.tq_chunk_workspace_bytes(c.handle, 1, 1, 1, 1, 2 ** 31 - 4096) > 0
+
+
+def test_one_workspace_for_smaller_calls(orc):
+    """A workspace sized for the largest step takes every step of as many sequences with fewer
+    queries or a smaller bound on the lengths, whatever way and split those would choose."""
+    import torch
+    tq = _tq()
+    for B, G, Hkv, most, top in ((1, 4, 2, 900, 4096), (2, 4, 1, 300, 1000), (1, 1, 1, 400, 256), (3, 8, 1, 200, 100)):
+        c = Case(orc, [1] * B, [top - 7 * b for b in range(B)], G, Hkv, seed=25)
+        g = torch.Generator(device="cuda").manual_seed(26)
+        ws = torch.full((tq.tq_chunk_workspace_bytes(c.c, B, most, G * Hkv, Hkv, top),), 0xFF, dtype=torch.uint8, device="cuda")
+        n = most
+        while n >= 1:
+            left = min(n, top - 7 * B)
+            c.nq = [left] + [min(n - left, 40)] * (B > 1) + [0] * (B - 2)
+            c.cu = torch.tensor([0] + list(np.cumsum(c.nq)), dtype=torch.int32, device="cuda")
+            c.q = (torch.randn((sum(c.nq), G * Hkv, 128), generator=g, device="cuda") / math.sqrt(128)).half()
+            assert tq.tq_chunk_workspace_bytes(c.c, B, n, G * Hkv, Hkv, top) > 0
+            out = c.run(ws=ws)
+            assert tq.tq_get_device_error(c.c) == 0
+            c.check(out, "chunk %d queries in a workspace for %d" % (n, most), heads=[0, G * Hkv - 1])
+            n = n * 2 // 3
+        # a smaller bound on the lengths
+        short = min(top, 90)
+        s = Case(orc, [2] * B, [short - b for b in range(B)], G, Hkv, seed=27)
+        s.check(s.run(ws=ws), "chunk short sequences in a workspace for long ones")
+    # and more than a pass of heads: half the bound fits more heads a pass than the whole one
+    c = gpu_ctx()
+    big = tq.tq_chunk_workspace_bytes(c, 1, 600, 6, 3, 1200000)
+    s = Case(orc, [300], [700], 2, 3, seed=28)
+    s.check(s.run(top=600000, ws=torch.empty(big, dtype=torch.uint8, device="cuda")), "chunk fewer heads a pass")
