@@ -18,7 +18,7 @@
 //   softmax warps  one thread per row: s = a_t D1 + b_t D2 in fp32 (the score's two scalars are
 //                  never rounded), mask, running maximum and sum, P to tensor memory.  With 32
 //                  rows four warps share a tile's tokens, 32 each, and P is the weight times
-//                  v_t: the maximum runs over s + log2 v_t, P = 2^(s + log2 v_t - m) <= 2^8
+//                  v_t: the maximum runs over s + log2 v_t, P = 2^(s + log2 v_t - m + 7) <= 2^15
 //                  whatever the values' size, and the sum takes P / v_t.  One rounding to fp16
 //                  instead of three (P, v_t, v_t c); with 128 rows, whose scalars do not fit
 //                  beside the tiles, the values' tile holds v_t c
@@ -74,11 +74,12 @@ struct FewSmem {
     static_assert(kOffK % 1024 == 0 && kBlock % 1024 == 0, "swizzled tiles");
 };
 constexpr uint64_t kFWaitNs = 2000000000ull;
-constexpr float kFRescale = 8.f;  // log2 of what P may grow to before O is rescaled
+constexpr float kFRescale = 8.f;  // log2 of what a weight may grow to before O is rescaled
+constexpr float kFPHeadroom = 7.f;  // log2 of P over the weight: fp16 loses weights below 2^-32 of the largest (attend_tc.cu)
 // ROWS = 32, where P carries the values' scalar v_t: a value below 2^-40 (a token's fp16 values, if
 // any is not 0, give 2^-29 at the least) counts as zero, and its P as if v_t were 2^-40.  That keeps
-// its weight in the sum: P is flushed below 2^-126, for such a token when its score is 86 - log2 v
-// below that of one of scalar v, a share of 2^-72 up to v = 2^14.
+// its weight in the sum: P is flushed below 2^-126, for such a token when its score is 93 - log2 v
+// below that of one of scalar v, a share of 2^-79 up to v = 2^14.
 constexpr float kFNoValue = 9.0949470177292824e-13f;
 constexpr uint32_t kFColS2 = 128, kFColO = 256, kFColP = 384;
 
@@ -579,7 +580,7 @@ __global__ void __launch_bounds__(FewSmem<ROWS>::kThreads, 1)
                 }
                 m = mn;
             }
-            const float mm = m == -INFINITY ? 0.f : m;
+            const float mm = m == -INFINITY ? 0.f : m - kFPHeadroom;
             const float2 nm = make_float2(-mm, -mm);
             uint32_t p[2 * kChunks][8];
 #pragma unroll

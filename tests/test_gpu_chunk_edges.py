@@ -199,3 +199,70 @@ def test_one_workspace_for_smaller_calls(orc):
     big = tq.tq_chunk_workspace_bytes(c, 1, 600, 6, 3, 1200000)
     s = Case(orc, [300], [700], 2, 3, seed=28)
     s.check(s.run(top=600000, ws=torch.empty(big, dtype=torch.uint8, device="cuda")), "chunk fewer heads a pass")
+
+
+@pytest.mark.parametrize("nq,G", WAYS)
+def test_many_small_weights_add_up(orc, nq, G):
+    """131072 tokens of weight 2^-26 beside one of weight 1: 0.2 % of the output, all of one sign.
+    Bound on the output's share along the small ones' value w, with o = u (the dominant token's
+    value) as the accumulator holds it, |u| |w| / |w|^2 of it along w:
+      * u's roundings: 2^-11 of it;
+      * the accumulator: an MMA adds 16 tokens, L / 16 additions, each truncated by up to 2^-23 of it;
+      * the sum that the output is divided by: at most L / 4 additions to the accumulator that
+        holds the large weight, each off by 2^-24 of it, times the output;
+      * the small weights: the score's error, and 2^-32 for each below P's least step.
+    Together two thirds of what the small weights give."""
+    import torch
+    L = 131072
+    # (as many CTAs as SMs, so that no sequence is split: a split without the first token has no small weights)
+    B, Hkv = (37, 4) if nq * G <= 128 else (1, 1)
+    c = Case(orc, [1], [32], G, Hkv, seed=29, spare=0)
+    kn, kg, vn = _scalars(c)
+    kn.zero_(), kg.zero_()
+    first, rest = (int(c.slots[0][t]) // 16 for t in (0, 16))
+    code, (vc0, vc1) = 64, (c.vc[first, 0], c.vc[rest, 0])
+    # one value for every small token, another of the same norm for the dominant one
+    for page in (vc0, vc1):
+        page[:16 * code] = page[:16 * code].view(16, code)[3].repeat(16)
+    vc0[code:16 * code] = vc1[code:16 * code]
+    vn[:] = 30.0
+    kn[first, 0, 0] = 4.0
+    c.kc[:], c.vc[:] = c.kc[:, :1].clone(), c.vc[:, :1].clone()  # every head alike
+    _refresh(c, orc)
+    u, w, key = c.V[0][0, 0], c.V[0][1, 0], c.K[0][0, 0]
+    c.bt = torch.full((B, L // 16), rest, dtype=torch.int32, device="cuda")
+    c.bt[:, 0] = first
+    c.top = L
+    c.L = torch.full((B,), L, dtype=torch.int32, device="cuda")
+    c.cu = torch.arange(B + 1, dtype=torch.int32, device="cuda") * nq
+    c.q = torch.empty((B * nq, G * Hkv, 128), dtype=torch.float16, device="cuda")
+    c.q[:] = (key / key.norm() * 3).half()
+    scale = 26 * math.log(2.0) / float(c.q[0, 0].double() @ key)
+    out = c.run(scale=scale).double()
+    small = (L - nq + torch.arange(nq, device="cuda")).repeat(B).double() * 2.0 ** -26  # all that each query sees but the first token
+    share = out @ w / (w @ w)
+    want = (float(u @ w / (w @ w)) + small) / (1 + small)
+    # (the score's error moves the small weights: 26 ln 2 times the bound of its rounding)
+    tol = (U16 + L / 16 * 2.0 ** -23) * float(u.abs() @ w.abs() / (w @ w)) + small * 26 * 4 * U16 + L * 2.0 ** -32
+    tol = tol + L / 4 * 2.0 ** -24 * want.abs()
+    assert bool((tol < 0.75 * small).all())
+    assert bool(((share - want[:, None]).abs() <= tol[:, None]).all()), float((share - want[:, None]).abs().max())
+
+
+def test_many_small_weights_add_up_prompt():
+    """The same over a prompt's exact values: a coordinate that the dominant token lacks."""
+    import torch
+    tq = _tq()
+    T = 30000
+    q, k = (torch.zeros((T, 1, 128), dtype=torch.float16, device="cuda") for _ in range(2))
+    v = torch.ones_like(k)
+    q[:, 0, 0], k[0, 0, 0], v[0, 0, 5] = 4.0, 4.0, 0.0
+    out = torch.empty((T, 1, 128), device="cuda")
+    tq.tq_prompt_attention(gpu_ctx(), q, k, v, torch.tensor([0, T], dtype=torch.int32, device="cuda"), out,
+                           scale=26 * math.log(2.0) / 16)
+    small = torch.arange(T, device="cuda").double() * 2.0 ** -26
+    want = small / (1 + small)
+    # the scale and the exponent's argument in fp32 (26 ln 2 each off by 2^-22), P in fp16 (its least step 2^-32)
+    tol = small * (26 * 2.0 ** -21 + U16) + T * 2.0 ** -33
+    err = (out[:, 0, 5].double() - want).abs()
+    assert bool((err <= tol).all()), float((err - tol).max())
