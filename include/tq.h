@@ -403,8 +403,8 @@ TQ_API size_t tq_chunk_workspace_bytes(const tq_ctx* ctx, int B, int total_q, in
  *   workspace_dev  : >= tq_chunk_workspace_bytes(...) bytes, 16-byte aligned; for this call or
  *                    for a larger one (see there).
  * A cache row behind a sequence's last token may hold anything, and a token's norms that are
- * not finite reach the queries that attend it only (for value norms up to 2^14 sqrt(d), beyond
- * which its values overflow fp16).  Three launches, or with many queries two or three for as
+ * not finite, or a value norm whose values pass fp16 (from 2^14 sqrt(d) on they may), reach
+ * the queries that attend it only.  Three launches, or with many queries two or three for as
  * many kv heads at a time as fit 1 GiB of decompressed tokens (one head at the least: 512
  * bytes a token of B sequences of max_seq_len), queued on stream, on the context's device;
  * total_q = 0 or B = 0 launches nothing.

@@ -111,6 +111,7 @@ struct FewArgs {
     LevelTable tk, tv;
     float qscale, sscale;    // scale log2(e) / sqrt(d) (times the key levels' scale), scale log2(e) sqrt(pi/2) / d
     float vscale;            // 1 / sqrt(d) times the value levels' scale
+    float vmost;             // the largest scalar whose product with every level of the table fits fp16
     const float* qfactor;    // [total_q * Hq] what q' and s of the row are to be multiplied by (a power of two)
     float* part;             // [splits][total_q * Hq][128] unscaled sums, rotated
     float2* ml;              // [splits][total_q * Hq] maximum (base 2) and sum
@@ -322,10 +323,10 @@ __global__ void __launch_bounds__(FewSmem<ROWS>::kThreads, 1)
             }
             fence_proxy_async_shared();
             mbar_arrive_lead(lead, bar(kFBKFull + s));
-            // the values of a token that is not finite are left out here and make the rows that
-            // attend it NaN at the end: a masked one must not reach any
+            // the values of a token that are not finite (with 128 rows: that pass fp16 in the tile) are
+            // left out here and make the rows that attend it NaN at the end: a masked one must not reach any
             const float vn = r.state ? 0.f : r.vn * a.vscale;
-            const bool fine = isfinite(vn);
+            const bool fine = fabsf(vn) <= (M::kWeighted ? 3.402823466e38f : a.vmost);
             if (!fine && sub == 0) atomicMin(first_bad, (j0 + j) * kFN + tok);
             const __half2 v2 = __float2half2_rn(fine ? vn : 0.f);
             const int vb = j % M::kVBufs, use = j / M::kVBufs;
@@ -928,6 +929,8 @@ cudaError_t launch_chunk_few(const tq_ctx* ctx, const ChunkPlan& plan, const Chu
     a.tv = ctx->levels_value;
     const float scale_log2 = c.scale * 1.4426950408889634f;
     a.vscale = a.tv.scale / std::sqrt((float)kDim);
+    // (scalar and level are each rounded up by 2^-11 at most: 65440 (1 + 2^-11)^2 < 65504)
+    a.vmost = 65440.f * a.tv.scale / ctx->cb_value.c[ctx->cb_value.levels - 1];
     a.qscale = scale_log2 * a.tk.scale / std::sqrt((float)kDim);
     a.sscale = scale_log2 * 1.2533141373155003f / (float)kDim;
     a.qfactor = factor;

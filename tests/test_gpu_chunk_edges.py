@@ -266,3 +266,21 @@ def test_many_small_weights_add_up_prompt():
     tol = small * (26 * 2.0 ** -21 + U16) + T * 2.0 ** -33
     err = (out[:, 0, 5].double() - want).abs()
     assert bool((err <= tol).all()), float((err - tol).max())
+
+
+@pytest.mark.parametrize("nq,G", WAYS)
+def test_values_beyond_fp16_reach_their_queries_only(orc, nq, G):
+    """A value norm whose coordinates pass fp16, of a token among the new ones: the queries before
+    it equal the run without it to the bit."""
+    import torch
+    c = Case(orc, [max(nq, 4), 2], [300, 40], G, 1, seed=30)
+    n = c.nq[0]
+    at = 300 - n // 2
+    ref = c.run()
+    vn = _scalars(c)[2]
+    slot = int(c.slots[0][at])
+    for norm in (2.0 ** 15 * math.sqrt(128), 2.0 ** 20, 1e38):
+        vn[slot // 16, 0, slot % 16] = norm
+        out = c.run()
+        first = at - (300 - n)
+        assert torch.equal(out[:first], ref[:first]) and torch.equal(out[n:], ref[n:])
