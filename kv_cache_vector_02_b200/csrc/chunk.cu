@@ -65,6 +65,7 @@ struct UnpackArgs {
     int num_blocks;
     const int32_t* block_table;
     int max_blocks;
+    const int32_t* cu_q;
     const int32_t* seq_lens;
     int B, max_kv, tiles;   // tiles per sequence, at most
     int Hkv, heads, head0;  // kv heads of the cache; of this launch
@@ -124,7 +125,8 @@ __global__ void __launch_bounds__(kUThreads, 1)
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
 
-    // items (sequence, tile, head), head fastest; those behind a sequence's last token are skipped
+    // items (sequence, tile, head), head fastest; those behind a sequence's last token are skipped,
+    // and sequences without queries
     const long long items = (long long)a.B * a.tiles * a.heads;
     struct Item {
         int b, j, h, len;
@@ -135,7 +137,7 @@ __global__ void __launch_bounds__(kUThreads, 1)
             it.h = (int)(i - bj * a.heads);
             it.b = (int)(bj / a.tiles);
             it.j = (int)(bj - (long long)it.b * a.tiles);
-            it.len = a.seq_lens[it.b];
+            it.len = a.cu_q[it.b + 1] > a.cu_q[it.b] ? a.seq_lens[it.b] : 0;
             if (it.len <= a.max_kv && it.j * kUN < it.len) return true;
             // on to this CTA's first item of the next sequence
             const long long left = (long long)(it.b + 1) * a.tiles * a.heads - i;
@@ -514,6 +516,7 @@ cudaError_t launch_chunk(const tq_ctx* ctx, const ChunkPlan& plan, const ChunkCa
     u.num_blocks = c.num_blocks;
     u.block_table = c.block_table;
     u.max_blocks = c.max_blocks;
+    u.cu_q = c.cu_q;
     u.seq_lens = c.seq_lens;
     u.B = c.B;
     u.max_kv = max_kv;

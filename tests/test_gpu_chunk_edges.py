@@ -284,3 +284,20 @@ def test_values_beyond_fp16_reach_their_queries_only(orc, nq, G):
         out = c.run()
         first = at - (300 - n)
         assert torch.equal(out[:first], ref[:first]) and torch.equal(out[n:], ref[n:])
+
+
+@pytest.mark.parametrize("nq,G", WAYS)
+def test_sequences_without_queries_are_not_looked_at(orc, nq, G):
+    """A batch filled up with empty sequences whose lengths and pages are left over."""
+    import torch
+    tq = _tq()
+    n = 4 * nq  # (the rows of a sequence on average choose the way)
+    c = Case(orc, [0, n, 0, 0], [40, 700, 90, 200], G, 2, seed=40)
+    ref = c.run()
+    c.check(ref, "chunk beside empty sequences")
+    bt = c.bt.clone()
+    bt[0], bt[2], bt[3] = -1, 10 ** 6, -5
+    for L in ([40, 700, 90, 200], [-7, 700, 10 ** 6, 704]):
+        out = c.run(block_table=bt, seq_lens=torch.tensor(L, dtype=torch.int32, device="cuda"))
+        assert tq.tq_get_device_error(c.c) == 0
+        assert torch.equal(out, ref)
