@@ -5,7 +5,7 @@ import math
 import numpy as np
 import pytest
 
-from attention64 import U16
+from attention64 import U16, attend64, rms_bound
 from parity import gpu_ctx
 from test_gpu_chunk import Case
 
@@ -301,3 +301,74 @@ def test_sequences_without_queries_are_not_looked_at(orc, nq, G):
         out = c.run(block_table=bt, seq_lens=torch.tensor(L, dtype=torch.int32, device="cuda"))
         assert tq.tq_get_device_error(c.c) == 0
         assert torch.equal(out, ref)
+
+
+@pytest.mark.parametrize("bits,km", [(4, 0), (3, 0), (2, 0), (4, 1), (3, 1), (2, 1)])
+@pytest.mark.parametrize("nq,G", WAYS)
+def test_every_width_on_every_way(orc, nq, G, bits, km):
+    c = Case(orc, [nq, 2], [400, 33], G, 2, bits, nq % 2, km, seed=31)
+    out = c.run()
+    assert _tq().tq_get_device_error(c.c) == 0
+    c.check(out, "chunk %d bits, mode %d, %d x %d rows" % (bits, km, nq, G))
+
+
+@pytest.mark.parametrize("B", [4, 12, 25, 40])
+def test_every_shape_of_the_join(orc, B):
+    """256, 768, 1600 and 2560 rows, the tokens split and not."""
+    c = Case(orc, [2] * B, [130 + 50 * (b % 5) for b in range(B)], 4, 8, seed=32)
+    c.check(c.run(), "chunk join of %d rows" % (64 * B), heads=[0, 13, 31])
+
+
+@pytest.mark.parametrize("nq,G,top,groups,split", [(300, 2, 800000, 2, True), (300, 2, 1200000, 3, True),
+                                                   (148, 128, 800000, 2, False)])
+def test_heads_in_passes(orc, nq, G, top, groups, split):
+    """More decompressed tokens than are held at a time, by the bound on the lengths: the kv heads
+    go in passes (2 + 1 and 1 + 1 + 1), with their tokens split over CTAs and not."""
+    import torch
+    tq = _tq()
+    c = Case(orc, [nq], [nq + 60], G, 3, seed=33)
+    n0 = tq.tq_launch_count()
+    out = c.run(top=top)
+    assert tq.tq_launch_count() - n0 == groups * (3 if split else 2)
+    assert tq.tq_get_device_error(c.c) == 0
+    c.check(out, "chunk heads in %d passes, G %d" % (groups, G))
+    bt = c.bt.clone()
+    bt[0, 1] = -1
+    skip = torch.zeros(nq + 60, dtype=torch.bool, device="cuda")
+    skip[16:32] = True
+    out = c.run(top=top, block_table=bt)
+    assert tq.tq_get_device_error(c.c) == tq.DEVERR_BLOCK
+    c.check(out, "chunk heads in passes, a page skipped", skip={0: skip})
+
+
+@pytest.mark.parametrize("nq,G", WAYS + [(300, 2)])
+def test_every_token_once_in_long_contexts(orc, nq, G):
+    """Each (query, head) looks at two tokens alone, out of 20011: its own, the last it may see,
+    and one at a border of tiles, both with a score of 25; the token behind its own would have 30.
+    A token left out, let in or counted twice moves an output by a sixth of
+    the two values' difference or more; the bound is six times the root mean square that
+    independent roundings give (attention64.py), about 4 % of a value."""
+    import torch
+    L = 20011
+    c = Case(orc, [nq], [L], G, 1, seed=34)
+    K, V = c.K[0][:, 0], c.V[0][:, 0]
+    own = L - nq + torch.arange(nq, device="cuda")
+    borders = torch.tensor([0, 127, 128, 255, 256, 639, 640, 1279, 1280, 2559, 2560, 5119, 5120, 10239, 10240, 19711, 19712],
+                           device="cuda")
+    behind = (own + 1).clamp(max=L - 1)
+    for h in range(G):
+        other = own if h == 0 else borders[(torch.arange(nq, device="cuda") * 5 + 3 * h) % len(borders)]
+        want = torch.full((nq, 3, 1), 25 * math.sqrt(128), dtype=torch.float64, device="cuda")
+        want[:, 2, 0] *= torch.where(own < L - 1, 1.2, 1.0)
+        c.q[:, h] = (torch.linalg.pinv(torch.stack([K[own], K[other], K[behind]], 1)) @ want)[..., 0].half()
+    out = c.run().double()
+    assert _tq().tq_get_device_error(c.c) == 0
+    for h in range(G):
+        o, A, _, _ = attend64(c.q[:, h:h + 1].double(), c.K[0], c.V[0], L - nq)
+        tol = 6 * rms_bound(A, c.q[:, h:h + 1].double(), c.K[0], 1) + L * 2.0 ** -25 * float(V.abs().max())
+        err = (out[:, h:h + 1] - o).abs()
+        assert bool((err <= tol).all()), (h, float((err / tol).max()))
+        # what the bound is worth: one token fewer (for each head's own), and one more, pass it by far
+        for first, rows in ((L - nq - 1, slice(None)), (L - nq + 1, slice(0, nq - 1))):
+            wrong = attend64(c.q[:, h:h + 1].double(), c.K[0], c.V[0], first)[0]
+            assert bool(((wrong - o).abs() > 2 * tol)[rows].flatten(1).any(1).all())
