@@ -268,6 +268,9 @@ TQ_API tq_status tq_decode_attention_window(const tq_ctx* ctx, const uint16_t* q
  *   scale          : softmax scale; 0 for the default 1/sqrt(d).
  *   out_dev        : [Tq][Hq][128], fp16 (out_fp32 = 0) or fp32 (out_fp32 = 1).
  * No workspace.  One kernel launch; Tq = 0 launches nothing.
+ * tq_chunk_attention computes the same for a batch of sequences, several times as fast (one
+ * of 4096 tokens, 32 query heads over 8: 259 us for 1619 with 4096 queries, 32 for 417 with
+ * 16), with a workspace and its keys or rotated queries rounded to fp16.
  */
 TQ_API tq_status tq_prefill_attention(const tq_ctx* ctx, const uint16_t* q_dev, const uint8_t* k_cache_dev,
                                       const uint8_t* v_cache_dev, int num_blocks, const int32_t* block_table_dev,
@@ -326,8 +329,8 @@ TQ_API tq_status tq_rope_plan(int rot_dim, int layout, double base, int scaling,
  *                  projection work as they are.  Either may be NULL (its heads are then not
  *                  looked at).  16-byte aligned.
  *   positions_dev: [T] int32; a negative position leaves the token's rows as they are (the
- *                  output's, if that is another buffer).  Any int32 position is exact to
- *                  2^-32 turns.
+ *                  output's, if that is another buffer).  The angle of any int32
+ *                  position is exact to 2^-26 turns (1e-7 rad, a float's rounding).
  *   q_out, k_out : as the inputs, with strides of their own.  An output may be its own
  *                  input (same address and stride); any other overlap among the inputs and
  *                  outputs is refused.
@@ -385,11 +388,13 @@ TQ_API size_t tq_chunk_workspace_bytes(const tq_ctx* ctx, int B, int total_q, in
  * its query i attends to the tokens 0 .. L_b - n_b + i:
  *   s_t = scale * ( <q_i, k_hat_t> + gamma_t*sqrt(pi/2)/d * <S q_i, 2 sigma_t - 1> ),
  *   o_i = sum_t softmax(s)_t * v_hat_t
- * (tq_prefill_attention's sums, for many sequences; the decompressed keys and values are
- * rounded to fp16).
+ * (tq_prefill_attention's sums, for many sequences; rounded to fp16 on the way are the
+ * decompressed keys and values, or the rotated queries where a sequence has few).
  *   q_dev          : [total_q][Hq][128] fp16, device, 16-byte aligned; Hq / Hkv 1 .. 128.
  *   cu_q_dev       : [B + 1] int32, non-decreasing, 0 .. total_q; as tq_prompt_attention's
- *                    cu_seqlens.  n_b = 0 is allowed.
+ *                    cu_seqlens (after TQ_DEVERR_SEQLEN for the list itself, any of the call's
+ *                    rows may hold anything).  n_b = 0 is allowed; such a sequence's length
+ *                    and pages are not looked at.
  *   num_blocks     : blocks of the caches, at least 1 (TQ_ERR_INVALID_ARG otherwise).
  *   block_table_dev: [B][max_blocks] int32.  A block id outside [0, num_blocks) skips the
  *                    page and sets TQ_DEVERR_BLOCK.

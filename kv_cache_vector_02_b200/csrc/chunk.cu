@@ -19,10 +19,20 @@
 // attention is one MMA per 16 coordinates instead of two (codes and signs).
 //
 // Which way: up to 128 (query, head of a group) rows a sequence on average, chunk_few.cu;
-// above, this one.  Measured on both sides (8 kv heads): 32 sequences of 3600 tokens with 18
-// rows, 145 us there and 305 here; pieces of 700 and 33 queries beside single tokens (490 rows
-// on average), 185 and 94; 2048 queries of 4096 tokens (8192 rows), 513 and 131; 256 queries of
-// 131072 tokens (2048 rows), 3140 and 1310.
+// above, this one.  Measured on both sides (32 heads over 8; us there and here), rows a sequence:
+//   32 sequences of 3600 tokens   32: 166, 287   64: 254, 288   128: 301, 292   192: 518, 312
+//   4 sequences of 2000           32: 34, 47     96: 45, 47     128: 47, 49     256: 68, 57
+//   1 sequence of 32768           32: 57, 103    64: 74, 107    128: 80, 108    256: 127, 117
+// 2048 queries of 4096 tokens (8192 rows), 513 and 131.  The average decides for the whole batch,
+// so a long piece among single tokens may go the slower way: 700 queries beside 31 single ones
+// over 2000 tokens each (91 rows on average), 240 and 195; 512 beside 31 over 4096 (68), 379 and
+// 342; 1000 beside 63 (66), 707 and 662.
+//
+// Roundings to fp16: R (one image of it, as the operand tiles leave no room for a second), the
+// levels (LevelTable) and the decompressed keys and values, which halves what the attention reads
+// and lets it be one MMA.  By a model of the arithmetic (4096 tokens, 64 bits but for the rounding
+// named; relative to the output): values 2.0e-4, R 2.0e-4, P 2.1e-4, keys 0.7e-4, levels 0.5e-4, an
+// fp16 output itself 2.1e-4.
 //
 // Bound: a tile of the decompression takes about 6500 cycles (HBM would allow 3750): its
 // lookups, MMAs and stores take turns on one set of operand tiles.  It is 12 us of the 131 above

@@ -24,12 +24,16 @@
 //                  beside the tiles, the values' tile holds v_t c
 // few_join_kernel     the splits joined, o = R acc / l in fp32
 //
-// Bound (32 sequences, 1 to 8 queries of 32 heads, about 3600 tokens each: 146 us, 1.0 TB/s of
-// pages; 135 of it in the attend kernel): the decoding.  A tile is about 8000 warp instructions
-// of lookups, two thirds of them on the ALU pipe at half rate, on the three sub-partitions that
-// the softmax leaves; a capture has the ALU pipe at 52 % over the whole kernel, the tensor pipe
-// at 38 %, DRAM at 13 %.  The MMAs of a tile, 24 of 65 cycles whatever the rows, would allow
-// 1560 cycles where it takes about 4000.  On the way: decompressing to fp16 first, 305 us; one
+// Roundings to fp16: q' and s, P, and what of the values the tile holds: the levels (LevelTable)
+// alone, or with 128 rows the scalar v_t and its product with the level too.
+//
+// Bound (32 sequences, 1 to 8 queries of 32 heads, about 3600 tokens each: 147 us, 1.0 TB/s of
+// pages; 130 of it in the attend kernel): a capture has the ALU pipe, the busiest, at 52 % over the
+// whole kernel, the issue slots at 52 %, the tensor pipe at 37 %, DRAM at 14 %; the counters do not
+// tell lookups from softmax and waiting.  The 16 decoding warps sit on three of the four
+// sub-partitions, six on one and five each on the others, and a tile is ready with the last of
+// them.  The MMAs of a tile, 24 of 65 cycles whatever the rows, would allow 1560 cycles where it
+// takes about 4000.  On the way: decompressing to fp16 first, 305 us; one
 // register set and one value buffer, 255; two of each up to 32 rows, 171; four softmax warps, 145.
 // Tried: four copies of the rows, one per lane quarter, each with its own softmax warp and a
 // single value buffer, 205; half of the exponentials by a polynomial, 149 against 148.
@@ -744,7 +748,7 @@ __global__ void __launch_bounds__(kRotThreads) few_rotate_kernel(const uint16_t*
 }
 
 // ---------------------------------------------------------------- joining and un-rotation
-// Two rows per warp: o = R (sum_s 2^(m_s - m) acc_s) / l.  R^T (fp32) in shared memory, a lane
+// PER rows per warp, WARPS of them per block: o = R (sum_s 2^(m_s - m) acc_s) / l.  R^T (fp32) in shared memory, a lane
 // takes four output coordinates.
 struct JoinArgs {
     const float* part;

@@ -6,9 +6,9 @@
 // turns by -a.
 //
 // Angles: the table holds theta_i / 2 pi as a 64-bit fraction of a turn, so pos * turns[i]
-// modulo 2^64 is the angle's fraction of a turn, exact up to pos * 2^-65 turns however far
-// the position is; 32 bits of it (a rounding of 2^-33 turns, 7e-10 rad) go into
-// sincospif.  A float product pos * theta would lose the angle from about 10^5 on.
+// modulo 2^64 is the angle's fraction of a turn, exact up to pos * 2^-64 turns however far
+// the position is.  32 bits of it go into sincospif as a float of 24: up to 2^-26 turns
+// (9.4e-8 rad) at half a turn, less for smaller angles.  A float product pos * theta would lose the angle from about 10^5 on.
 //
 // Bound by HBM: every value is read and written once.  A block takes one token (a few where
 // they are small): its threads first issue the 16-byte loads of two units each (a unit: 8 pairs in the
