@@ -86,19 +86,6 @@ enum : int {
     kANumBars = 24
 };
 
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
-// The largest of three; NaN if one is.
-__device__ __forceinline__ float max3(float x, float y, float z) {
-    float m;
-    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(m) : "f"(x), "f"(y), "f"(z));
-    return m;
-}
-
 // V as the B operand: [token][64 coordinates] rows of 128 bytes, 128-byte swizzle, the
 // coordinates (N) contiguous.  LBO: from one 64-coordinate block to the next; SBO: from
 // one 8-token group to the next.

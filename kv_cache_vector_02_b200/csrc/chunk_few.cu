@@ -124,18 +124,6 @@ struct FewArgs {
     uint32_t* err;
 };
 
-__device__ __forceinline__ float few_ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-// The largest of three; NaN if one is.
-__device__ __forceinline__ float few_max3(float x, float y, float z) {
-    float m;
-    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(m) : "f"(x), "f"(y), "f"(z));
-    return m;
-}
-
 // Named barriers of n threads: whether x holds in any of them; plain.
 __device__ __forceinline__ bool any_of_threads(int id, int n, bool x) {
     uint32_t r;
@@ -379,273 +367,273 @@ __global__ void __launch_bounds__(FewSmem<ROWS>::kThreads, 1)
     } else if (!softmax) {
         if (ROWS != 32) set_registers_down<kFIssueRegs>();
         if (warp == kWarpIssue) {
-        // ------------------------------------------------------------ MMA issuer (converged warp)
-        constexpr uint32_t id_s = idesc_f16(128, kFN), id_o = idesc_f16(128, kDim) | (1u << 16);
-        const uint32_t lead = elect_lane();
-        const uint32_t q_lo = sw128_desc_lo(sbase + M::kOffQ), k_lo = sw128_desc_lo(sbase + M::kOffK);
-        // the values as they lie, N-major: 64-coordinate blocks kFHalf apart
-        const uint32_t v_lo = (((sbase + M::kOffV) >> 4) & 0x3FFFu) | ((kFHalf >> 4) << 16);
-        auto wait = [&](int i, int phase) -> bool {
-            if (mbar_wait_all(bar(i), (uint32_t)phase & 1u, abort, kFWaitNs)) return true;
-            if (lane == 0) give_up();
-            return false;
-        };
-        auto values = [&](int j) {
+            // ------------------------------------------------------------ MMA issuer (converged warp)
+            constexpr uint32_t id_s = idesc_f16(128, kFN), id_o = idesc_f16(128, kDim) | (1u << 16);
+            const uint32_t lead = elect_lane();
+            const uint32_t q_lo = sw128_desc_lo(sbase + M::kOffQ), k_lo = sw128_desc_lo(sbase + M::kOffK);
+            // the values as they lie, N-major: 64-coordinate blocks kFHalf apart
+            const uint32_t v_lo = (((sbase + M::kOffV) >> 4) & 0x3FFFu) | ((kFHalf >> 4) << 16);
+            auto wait = [&](int i, int phase) -> bool {
+                if (mbar_wait_all(bar(i), (uint32_t)phase & 1u, abort, kFWaitNs)) return true;
+                if (lane == 0) give_up();
+                return false;
+            };
+            auto values = [&](int j) {
 #pragma unroll
-            for (int ks = 0; ks < 8; ++ks)
-                umma_ts_warp(lead, kFColO, kFColP + ks * 8, sw128_desc(v_lo + (j % M::kVBufs) * (kFTile >> 4) + ks * (2048 >> 4)),
-                             id_o, (j | ks) > 0);
-            umma_commit_warp(lead, bar(kFBO));
-            umma_commit_warp(lead, bar(kFBVEmpty + j % M::kVBufs));
-        };
-        bool ok = tmem == 0;
-        if (!ok && lane == 0) {
-            *abort = 1;
-            atomicOr(a.err, TQ_DEVERR_INTERNAL);
-        }
-        ok = ok && wait(kFBQ, 0);
-        for (int j = 0; ok && j < n; ++j) {
-            ok = wait(kFBKFull + (j & 1), j / 2) && (j == 0 || wait(kFBL, j - 1));
-            if (!ok) break;
-            tc_fence_after();
-            const uint32_t kl = k_lo + (j & 1) * (2 * kFTile >> 4);
-#pragma unroll
-            for (int ks = 0; ks < 8; ++ks) {
-                const uint32_t o = (uint32_t)(ks & 3) * 2 + (uint32_t)(ks >> 2) * (kFHalf >> 4);
-                const uint32_t qo = (uint32_t)(ks & 3) * 2 + (uint32_t)(ks >> 2) * (M::kBlock >> 4);
-                umma_ss_warp(lead, 0, sw128_desc(q_lo + qo), sw128_desc(kl + o), id_s, ks > 0);
-                if (PROD)
-                    umma_ss_warp(lead, kFColS2, sw128_desc(q_lo + (2 * M::kBlock >> 4) + qo),
-                                 sw128_desc(kl + (kFTile >> 4) + o), id_s, ks > 0);
+                for (int ks = 0; ks < 8; ++ks)
+                    umma_ts_warp(lead, kFColO, kFColP + ks * 8, sw128_desc(v_lo + (j % M::kVBufs) * (kFTile >> 4) + ks * (2048 >> 4)),
+                                 id_o, (j | ks) > 0);
+                umma_commit_warp(lead, bar(kFBO));
+                umma_commit_warp(lead, bar(kFBVEmpty + j % M::kVBufs));
+            };
+            bool ok = tmem == 0;
+            if (!ok && lane == 0) {
+                *abort = 1;
+                atomicOr(a.err, TQ_DEVERR_INTERNAL);
             }
-            umma_commit_warp(lead, bar(kFBS));
-            umma_commit_warp(lead, bar(kFBKEmpty + (j & 1)));
-            if (j > 0) {
-                ok = wait(kFBP, j - 1) && wait(kFBVFull + (j - 1) % M::kVBufs, (j - 1) / M::kVBufs);
+            ok = ok && wait(kFBQ, 0);
+            for (int j = 0; ok && j < n; ++j) {
+                ok = wait(kFBKFull + (j & 1), j / 2) && (j == 0 || wait(kFBL, j - 1));
                 if (!ok) break;
                 tc_fence_after();
-                values(j - 1);
+                const uint32_t kl = k_lo + (j & 1) * (2 * kFTile >> 4);
+#pragma unroll
+                for (int ks = 0; ks < 8; ++ks) {
+                    const uint32_t o = (uint32_t)(ks & 3) * 2 + (uint32_t)(ks >> 2) * (kFHalf >> 4);
+                    const uint32_t qo = (uint32_t)(ks & 3) * 2 + (uint32_t)(ks >> 2) * (M::kBlock >> 4);
+                    umma_ss_warp(lead, 0, sw128_desc(q_lo + qo), sw128_desc(kl + o), id_s, ks > 0);
+                    if (PROD)
+                        umma_ss_warp(lead, kFColS2, sw128_desc(q_lo + (2 * M::kBlock >> 4) + qo),
+                                     sw128_desc(kl + (kFTile >> 4) + o), id_s, ks > 0);
+                }
+                umma_commit_warp(lead, bar(kFBS));
+                umma_commit_warp(lead, bar(kFBKEmpty + (j & 1)));
+                if (j > 0) {
+                    ok = wait(kFBP, j - 1) && wait(kFBVFull + (j - 1) % M::kVBufs, (j - 1) / M::kVBufs);
+                    if (!ok) break;
+                    tc_fence_after();
+                    values(j - 1);
+                }
             }
-        }
-        if (ok) ok = wait(kFBP, n - 1) && wait(kFBVFull + (n - 1) % M::kVBufs, (n - 1) / M::kVBufs);
-        if (ok) {
-            tc_fence_after();
-            values(n - 1);
-        }
-        umma_commit_warp(lead, bar(kFBDrain));
-        const volatile int never = 0;
-        mbar_wait(bar(kFBQ), 0, &never, kFWaitNs);
-        mbar_wait(bar(kFBDrain), 0, &never, kFWaitNs);
-        __syncwarp();
+            if (ok) ok = wait(kFBP, n - 1) && wait(kFBVFull + (n - 1) % M::kVBufs, (n - 1) / M::kVBufs);
+            if (ok) {
+                tc_fence_after();
+                values(n - 1);
+            }
+            umma_commit_warp(lead, bar(kFBDrain));
+            const volatile int never = 0;
+            mbar_wait(bar(kFBQ), 0, &never, kFWaitNs);
+            mbar_wait(bar(kFBDrain), 0, &never, kFWaitNs);
+            __syncwarp();
         }
     } else {
         if (ROWS != 32) set_registers_up<kFSoftmaxRegs>();
         if (ROWS == 32 || warp < live_warps) {
-        // ------------------------------------------------------------ softmax
-        constexpr int kCols = kFN / kParts, kChunks = kCols / 32;  // tokens of this thread
-        const int part = ROWS == 32 ? warp / 4 : 0, row = ROWS == 32 ? lane : (int)threadIdx.x;
-        const uint32_t lanes = ROWS == 32 ? 0u : (uint32_t)warp << 21, lead = lane == 0;
-        const uint32_t ts = tmem + lanes + kCols * part, tp = tmem + kFColP + kCols / 2 * part + lanes;
-        const uint32_t to = tmem + kFColO + kCols * part + lanes;
-        const bool live = row < nrows;
-        const int limit = live ? off + q0 + row / a.G - j0 * kFN : -1;  // its last token, from the split's first
-        const int masked_from = (off + q0 + 1) / kFN - j0;             // first tile with a masked pair
-        float* tops = reinterpret_cast<float*>(smem + M::kOffTop) + lane;  // [kParts][32]
-        // D1 and D2 are 1 / fac of the row's products.  With 32 rows the scores of a warp that has
-        // such a row are put right as they come; with 128 the exponent's argument takes the factor.
-        const float fac = live ? a.qfactor[out_row(row)] : 1.f;
-        const float rest = M::kWeighted ? 1.f : fac;
-        const bool scaled = __any_sync(0xffffffffu, fac != 1.f) != 0;
-        float m = -INFINITY;
-        float2 sum[2] = {{0.f, 0.f}, {0.f, 0.f}};
-        bool ok = true;
-        // after a wait that gave up the loop goes on without waiting: the parts' barriers need every warp
-        auto wait = [&](int x, int phase) {
-            if (ok && !mbar_wait_all(bar(x), (uint32_t)phase & 1u, abort, kFWaitNs)) {
-                give_up();
-                ok = false;
-            }
-        };
-        for (int j = 0; j < n; ++j) {
-            wait(kFBS, j);
-            tc_fence_after();
-            uint32_t s[kChunks][32];
-            const float4* sc = reinterpret_cast<const float4*>(smem + M::kOffScal + (j & 1) * (M::kScalars * 512)) + kCols / 4 * part;
+            // ------------------------------------------------------------ softmax
+            constexpr int kCols = kFN / kParts, kChunks = kCols / 32;  // tokens of this thread
+            const int part = ROWS == 32 ? warp / 4 : 0, row = ROWS == 32 ? lane : (int)threadIdx.x;
+            const uint32_t lanes = ROWS == 32 ? 0u : (uint32_t)warp << 21, lead = lane == 0;
+            const uint32_t ts = tmem + lanes + kCols * part, tp = tmem + kFColP + kCols / 2 * part + lanes;
+            const uint32_t to = tmem + kFColO + kCols * part + lanes;
+            const bool live = row < nrows;
+            const int limit = live ? off + q0 + row / a.G - j0 * kFN : -1;  // its last token, from the split's first
+            const int masked_from = (off + q0 + 1) / kFN - j0;             // first tile with a masked pair
+            float* tops = reinterpret_cast<float*>(smem + M::kOffTop) + lane;  // [kParts][32]
+            // D1 and D2 are 1 / fac of the row's products.  With 32 rows the scores of a warp that has
+            // such a row are put right as they come; with 128 the exponent's argument takes the factor.
+            const float fac = live ? a.qfactor[out_row(row)] : 1.f;
+            const float rest = M::kWeighted ? 1.f : fac;
+            const bool scaled = __any_sync(0xffffffffu, fac != 1.f) != 0;
+            float m = -INFINITY;
+            float2 sum[2] = {{0.f, 0.f}, {0.f, 0.f}};
+            bool ok = true;
+            // after a wait that gave up the loop goes on without waiting: the parts' barriers need every warp
+            auto wait = [&](int x, int phase) {
+                if (ok && !mbar_wait_all(bar(x), (uint32_t)phase & 1u, abort, kFWaitNs)) {
+                    give_up();
+                    ok = false;
+                }
+            };
+            for (int j = 0; j < n; ++j) {
+                wait(kFBS, j);
+                tc_fence_after();
+                uint32_t s[kChunks][32];
+                const float4* sc = reinterpret_cast<const float4*>(smem + M::kOffScal + (j & 1) * (M::kScalars * 512)) + kCols / 4 * part;
 #pragma unroll
-            for (int q = 0; q < 2 * kChunks; ++q) {  // 16 tokens
-                uint32_t d1[16], d2[16];
-                tmem_ld16(ts + 16 * q, d1);
-                if (PROD) tmem_ld16(ts + kFColS2 + 16 * q, d2);
-                tmem_ld_wait();
+                for (int q = 0; q < 2 * kChunks; ++q) {  // 16 tokens
+                    uint32_t d1[16], d2[16];
+                    tmem_ld16(ts + 16 * q, d1);
+                    if (PROD) tmem_ld16(ts + kFColS2 + 16 * q, d2);
+                    tmem_ld_wait();
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {  // four tokens
-                    const float4 fa = sc[4 * q + e];
-                    uint32_t* x = &s[q / 2][16 * (q & 1) + 4 * e];
-                    const uint32_t* z = &d1[4 * e];
-                    // (-0: nothing added)
-                    const float4 fl = M::kWeighted ? sc[64 + 4 * q + e] : make_float4(-0.f, -0.f, -0.f, -0.f);
-                    const float2 z01 = make_float2(__uint_as_float(z[0]), __uint_as_float(z[1]));
-                    const float2 z23 = make_float2(__uint_as_float(z[2]), __uint_as_float(z[3]));
-                    float2 u = __ffma2_rn(make_float2(fa.x, fa.y), z01, make_float2(fl.x, fl.y));
-                    float2 v = __ffma2_rn(make_float2(fa.z, fa.w), z23, make_float2(fl.z, fl.w));
-                    if (PROD) {
-                        const float4 fb = sc[32 + 4 * q + e];
-                        const uint32_t* y = &d2[4 * e];
-                        u = __ffma2_rn(make_float2(fb.x, fb.y), make_float2(__uint_as_float(y[0]), __uint_as_float(y[1])), u);
-                        v = __ffma2_rn(make_float2(fb.z, fb.w), make_float2(__uint_as_float(y[2]), __uint_as_float(y[3])), v);
+                    for (int e = 0; e < 4; ++e) {  // four tokens
+                        const float4 fa = sc[4 * q + e];
+                        uint32_t* x = &s[q / 2][16 * (q & 1) + 4 * e];
+                        const uint32_t* z = &d1[4 * e];
+                        // (-0: nothing added)
+                        const float4 fl = M::kWeighted ? sc[64 + 4 * q + e] : make_float4(-0.f, -0.f, -0.f, -0.f);
+                        const float2 z01 = make_float2(__uint_as_float(z[0]), __uint_as_float(z[1]));
+                        const float2 z23 = make_float2(__uint_as_float(z[2]), __uint_as_float(z[3]));
+                        float2 u = __ffma2_rn(make_float2(fa.x, fa.y), z01, make_float2(fl.x, fl.y));
+                        float2 v = __ffma2_rn(make_float2(fa.z, fa.w), z23, make_float2(fl.z, fl.w));
+                        if (PROD) {
+                            const float4 fb = sc[32 + 4 * q + e];
+                            const uint32_t* y = &d2[4 * e];
+                            u = __ffma2_rn(make_float2(fb.x, fb.y), make_float2(__uint_as_float(y[0]), __uint_as_float(y[1])), u);
+                            v = __ffma2_rn(make_float2(fb.z, fb.w), make_float2(__uint_as_float(y[2]), __uint_as_float(y[3])), v);
+                        }
+                        x[0] = __float_as_uint(u.x);
+                        x[1] = __float_as_uint(u.y);
+                        x[2] = __float_as_uint(v.x);
+                        x[3] = __float_as_uint(v.y);
                     }
-                    x[0] = __float_as_uint(u.x);
-                    x[1] = __float_as_uint(u.y);
-                    x[2] = __float_as_uint(v.x);
-                    x[3] = __float_as_uint(v.y);
                 }
-            }
-            if (M::kWeighted && scaled) {  // (seldom)
-                // a rounding of log2 v_t is multiplied too: 2^-24 |log2 v_t| fac, at most 2^-15 |log2 v_t|
+                if (M::kWeighted && scaled) {  // (seldom)
+                    // a rounding of log2 v_t is multiplied too: 2^-24 |log2 v_t| fac, at most 2^-15 |log2 v_t|
 #pragma unroll
-                for (int q = 0; q < kCols / 4; ++q) {
-                    const float4 fl = sc[64 + q];
-                    uint32_t* x = &s[q / 8][4 * (q % 8)];
-                    x[0] = __float_as_uint(fmaf(__uint_as_float(x[0]) - fl.x, fac, fl.x));
-                    x[1] = __float_as_uint(fmaf(__uint_as_float(x[1]) - fl.y, fac, fl.y));
-                    x[2] = __float_as_uint(fmaf(__uint_as_float(x[2]) - fl.z, fac, fl.z));
-                    x[3] = __float_as_uint(fmaf(__uint_as_float(x[3]) - fl.w, fac, fl.w));
+                    for (int q = 0; q < kCols / 4; ++q) {
+                        const float4 fl = sc[64 + q];
+                        uint32_t* x = &s[q / 8][4 * (q % 8)];
+                        x[0] = __float_as_uint(fmaf(__uint_as_float(x[0]) - fl.x, fac, fl.x));
+                        x[1] = __float_as_uint(fmaf(__uint_as_float(x[1]) - fl.y, fac, fl.y));
+                        x[2] = __float_as_uint(fmaf(__uint_as_float(x[2]) - fl.z, fac, fl.z));
+                        x[3] = __float_as_uint(fmaf(__uint_as_float(x[3]) - fl.w, fac, fl.w));
+                    }
                 }
-            }
-            const uint2 pb = *reinterpret_cast<const uint2*>(page_bad + 8 * (j & 1));
-            tc_fence_before();
-            mbar_arrive_lead(lead, bar(kFBL));
-            if (!M::kWeighted) mbar_arrive_lead(lead, bar(kFBKEmpty + (j & 1)));
-            if (j >= masked_from) {
-                const int lim = limit - j * kFN - kCols * part;
+                const uint2 pb = *reinterpret_cast<const uint2*>(page_bad + 8 * (j & 1));
+                tc_fence_before();
+                mbar_arrive_lead(lead, bar(kFBL));
+                if (!M::kWeighted) mbar_arrive_lead(lead, bar(kFBKEmpty + (j & 1)));
+                if (j >= masked_from) {
+                    const int lim = limit - j * kFN - kCols * part;
 #pragma unroll
-                for (int q = 0; q < kChunks; ++q)
+                    for (int q = 0; q < kChunks; ++q)
 #pragma unroll
-                    for (int e = 0; e < 32; ++e)
-                        if (32 * q + e > lim) s[q][e] = 0xFF800000u;  // -inf
-            }
-            if (pb.x | pb.y) {
+                        for (int e = 0; e < 32; ++e)
+                            if (32 * q + e > lim) s[q][e] = 0xFF800000u;  // -inf
+                }
+                if (pb.x | pb.y) {
+#pragma unroll
+                    for (int q = 0; q < kChunks; ++q) {
+                        const int page = 2 * (kChunks * part + q);  // the chunk's first of the tile's eight
+                        const uint32_t w = (page < 4 ? pb.x : pb.y) >> (8 * (page & 3));
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            if ((w >> (8 * (e / 16))) & 1u) s[q][e] = 0xFF800000u;
+                    }
+                }
+                float top = -INFINITY;
 #pragma unroll
                 for (int q = 0; q < kChunks; ++q) {
-                    const int page = 2 * (kChunks * part + q);  // the chunk's first of the tile's eight
-                    const uint32_t w = (page < 4 ? pb.x : pb.y) >> (8 * (page & 3));
+                    float m0 = max3(__uint_as_float(s[q][0]), __uint_as_float(s[q][1]), __uint_as_float(s[q][2]));
+                    float m1 = max3(__uint_as_float(s[q][16]), __uint_as_float(s[q][17]), __uint_as_float(s[q][18]));
 #pragma unroll
-                    for (int e = 0; e < 32; ++e)
-                        if ((w >> (8 * (e / 16))) & 1u) s[q][e] = 0xFF800000u;
+                    for (int e = 3; e < 15; e += 2) {
+                        m0 = max3(m0, __uint_as_float(s[q][e]), __uint_as_float(s[q][e + 1]));
+                        m1 = max3(m1, __uint_as_float(s[q][16 + e]), __uint_as_float(s[q][17 + e]));
+                    }
+                    top = max3(top, max3(m0, m0, __uint_as_float(s[q][15])), max3(m1, m1, __uint_as_float(s[q][31])));
                 }
-            }
-            float top = -INFINITY;
+                if (!M::kWeighted) top *= rest;
+                // a NaN or infinite score makes the row's sum and outputs NaN; the maximum carries it
+                if (!(top < INFINITY)) top = NAN;
+                auto grows = [&](float t) { return t > m + kFRescale || (m == -INFINITY && t > m) || (t != t && m == m); };
+                bool any = grows(top);
+                any = kParts > 1 ? any_of_threads(1, 32 * kParts, any) : __any_sync(0xffffffffu, any) != 0;
+                if (any) {
+                    if (kParts > 1) {
+                        tops[32 * part] = top;
+                        sync_threads(1, 32 * kParts);
 #pragma unroll
-            for (int q = 0; q < kChunks; ++q) {
-                float m0 = few_max3(__uint_as_float(s[q][0]), __uint_as_float(s[q][1]), __uint_as_float(s[q][2]));
-                float m1 = few_max3(__uint_as_float(s[q][16]), __uint_as_float(s[q][17]), __uint_as_float(s[q][18]));
+                        for (int i = 0; i < kParts; ++i) top = max3(top, top, tops[32 * i]);
+                        sync_threads(1, 32 * kParts);
+                    }
+                    const bool grow = grows(top);
+                    const float mn = grow ? top : m;
+                    if (j > 0) {
+                        const float f = grow ? ex2(m - mn) : 1.f;  // (first maximum: ex2(-inf) = 0)
 #pragma unroll
-                for (int e = 3; e < 15; e += 2) {
-                    m0 = few_max3(m0, __uint_as_float(s[q][e]), __uint_as_float(s[q][e + 1]));
-                    m1 = few_max3(m1, __uint_as_float(s[q][16 + e]), __uint_as_float(s[q][17 + e]));
-                }
-                top = few_max3(top, few_max3(m0, m0, __uint_as_float(s[q][15])), few_max3(m1, m1, __uint_as_float(s[q][31])));
-            }
-            if (!M::kWeighted) top *= rest;
-            // a NaN or infinite score makes the row's sum and outputs NaN; the maximum carries it
-            if (!(top < INFINITY)) top = NAN;
-            auto grows = [&](float t) { return t > m + kFRescale || (m == -INFINITY && t > m) || (t != t && m == m); };
-            bool any = grows(top);
-            any = kParts > 1 ? any_of_threads(1, 32 * kParts, any) : __any_sync(0xffffffffu, any) != 0;
-            if (any) {
-                if (kParts > 1) {
-                    tops[32 * part] = top;
-                    sync_threads(1, 32 * kParts);
-#pragma unroll
-                    for (int i = 0; i < kParts; ++i) top = few_max3(top, top, tops[32 * i]);
-                    sync_threads(1, 32 * kParts);
-                }
-                const bool grow = grows(top);
-                const float mn = grow ? top : m;
-                if (j > 0) {
-                    const float f = grow ? few_ex2(m - mn) : 1.f;  // (first maximum: ex2(-inf) = 0)
-#pragma unroll
-                    for (int q = 0; q < 2; ++q) sum[q] = __fmul2_rn(sum[q], make_float2(f, f));
-                    wait(kFBO, j - 1);  // the tile before is in O
-                    tc_fence_after();
+                        for (int q = 0; q < 2; ++q) sum[q] = __fmul2_rn(sum[q], make_float2(f, f));
+                        wait(kFBO, j - 1);  // the tile before is in O
+                        tc_fence_after();
 #pragma unroll 1
-                    for (int q = 0; q < 2 * kChunks; ++q) {
-                        uint32_t o[16];
-                        tmem_ld16(to + 16 * q, o);
-                        tmem_ld_wait();
-                        uint32_t lo[8], hi[8];
+                        for (int q = 0; q < 2 * kChunks; ++q) {
+                            uint32_t o[16];
+                            tmem_ld16(to + 16 * q, o);
+                            tmem_ld_wait();
+                            uint32_t lo[8], hi[8];
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            lo[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                            hi[e] = __float_as_uint(__uint_as_float(o[8 + e]) * f);
+                            for (int e = 0; e < 8; ++e) {
+                                lo[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                                hi[e] = __float_as_uint(__uint_as_float(o[8 + e]) * f);
+                            }
+                            tmem_st8(to + 16 * q, lo);
+                            tmem_st8(to + 16 * q + 8, hi);
                         }
-                        tmem_st8(to + 16 * q, lo);
-                        tmem_st8(to + 16 * q + 8, hi);
+                    }
+                    m = mn;
+                }
+                const float mm = m == -INFINITY ? 0.f : m - kFPHeadroom;
+                const float2 nm = make_float2(-mm, -mm);
+                uint32_t p[2 * kChunks][8];
+#pragma unroll
+                for (int q = 0; q < 2 * kChunks; ++q) {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const int i = 16 * q + 2 * e;
+                        float2 x = make_float2(__uint_as_float(s[i / 32][i % 32]), __uint_as_float(s[i / 32][i % 32 + 1]));
+                        x = M::kWeighted ? __fadd2_rn(x, nm) : __ffma2_rn(x, make_float2(rest, rest), nm);
+                        x.x = ex2(x.x);
+                        x.y = ex2(x.y);
+                        if (M::kWeighted) {  // the weight in the sum is without the value's scalar
+                            const float2 iv = reinterpret_cast<const float2*>(sc + 96)[8 * q + e];
+                            sum[e & 1] = __ffma2_rn(x, iv, sum[e & 1]);
+                        } else {
+                            sum[e & 1] = __fadd2_rn(sum[e & 1], x);
+                        }
+                        const __half2 hp = __floats2half2_rn(x.x, x.y);
+                        p[q][e] = *reinterpret_cast<const uint32_t*>(&hp);
                     }
                 }
-                m = mn;
+                if (M::kWeighted) mbar_arrive_lead(lead, bar(kFBKEmpty + (j & 1)));  // its scalars are read
+                // the tile before's P has been read
+                if (j > 0 && !any) wait(kFBO, j - 1);
+#pragma unroll
+                for (int q = 0; q < 2 * kChunks; ++q) tmem_st8(tp + 8 * q, p[q]);
+                tmem_st_wait();
+                tc_fence_before();
+                mbar_arrive_lead(lead, bar(kFBP));
             }
-            const float mm = m == -INFINITY ? 0.f : m - kFPHeadroom;
-            const float2 nm = make_float2(-mm, -mm);
-            uint32_t p[2 * kChunks][8];
+            wait(kFBO, n - 1);
+            float l = (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+            if (kParts > 1) {  // the row's sum: the same terms in the same order in every part
+                tops[32 * part] = l;
+                sync_threads(1, 32 * kParts);
+                l = 0.f;
 #pragma unroll
-            for (int q = 0; q < 2 * kChunks; ++q) {
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const int i = 16 * q + 2 * e;
-                    float2 x = make_float2(__uint_as_float(s[i / 32][i % 32]), __uint_as_float(s[i / 32][i % 32 + 1]));
-                    x = M::kWeighted ? __fadd2_rn(x, nm) : __ffma2_rn(x, make_float2(rest, rest), nm);
-                    x.x = few_ex2(x.x);
-                    x.y = few_ex2(x.y);
-                    if (M::kWeighted) {  // the weight in the sum is without the value's scalar
-                        const float2 iv = reinterpret_cast<const float2*>(sc + 96)[8 * q + e];
-                        sum[e & 1] = __ffma2_rn(x, iv, sum[e & 1]);
-                    } else {
-                        sum[e & 1] = __fadd2_rn(sum[e & 1], x);
-                    }
-                    const __half2 hp = __floats2half2_rn(x.x, x.y);
-                    p[q][e] = *reinterpret_cast<const uint32_t*>(&hp);
-                }
+                for (int i = 0; i < kParts; ++i) l += tops[32 * i];
             }
-            if (M::kWeighted) mbar_arrive_lead(lead, bar(kFBKEmpty + (j & 1)));  // its scalars are read
-            // the tile before's P has been read
-            if (j > 0 && !any) wait(kFBO, j - 1);
-#pragma unroll
-            for (int q = 0; q < 2 * kChunks; ++q) tmem_st8(tp + 8 * q, p[q]);
-            tmem_st_wait();
-            tc_fence_before();
-            mbar_arrive_lead(lead, bar(kFBP));
-        }
-        wait(kFBO, n - 1);
-        float l = (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
-        if (kParts > 1) {  // the row's sum: the same terms in the same order in every part
-            tops[32 * part] = l;
-            sync_threads(1, 32 * kParts);
-            l = 0.f;
-#pragma unroll
-            for (int i = 0; i < kParts; ++i) l += tops[32 * i];
-        }
-        const size_t prow = live ? prow0 + out_row(row) : 0;
-        if (live && part == 0) {
-            const bool hit = limit + j0 * kFN >= *reinterpret_cast<volatile int*>(first_bad);
-            a.ml[prow] = ok ? make_float2(m, hit ? NAN : l) : make_float2(-INFINITY, 0.f);
-        }
-        if (ok) {
-            tc_fence_after();
+            const size_t prow = live ? prow0 + out_row(row) : 0;
+            if (live && part == 0) {
+                const bool hit = limit + j0 * kFN >= *reinterpret_cast<volatile int*>(first_bad);
+                a.ml[prow] = ok ? make_float2(m, hit ? NAN : l) : make_float2(-INFINITY, 0.f);
+            }
+            if (ok) {
+                tc_fence_after();
 #pragma unroll 1
-            for (int q = 0; q < kChunks; ++q) {
-                uint32_t o[32];
-                tmem_ld32(to + 32 * q, o);
-                tmem_ld_wait();
-                if (!live) continue;
-                float4* d = reinterpret_cast<float4*>(a.part + prow * kDim + kCols * part + 32 * q);
+                for (int q = 0; q < kChunks; ++q) {
+                    uint32_t o[32];
+                    tmem_ld32(to + 32 * q, o);
+                    tmem_ld_wait();
+                    if (!live) continue;
+                    float4* d = reinterpret_cast<float4*>(a.part + prow * kDim + kCols * part + 32 * q);
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    d[i] = make_float4(__uint_as_float(o[4 * i]), __uint_as_float(o[4 * i + 1]),
-                                       __uint_as_float(o[4 * i + 2]), __uint_as_float(o[4 * i + 3]));
+                    for (int i = 0; i < 8; ++i)
+                        d[i] = make_float4(__uint_as_float(o[4 * i]), __uint_as_float(o[4 * i + 1]),
+                                           __uint_as_float(o[4 * i + 2]), __uint_as_float(o[4 * i + 3]));
+                }
+                tc_fence_before();
             }
-            tc_fence_before();
-        }
         }
     }
     __syncthreads();
