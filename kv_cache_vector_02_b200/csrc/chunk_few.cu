@@ -736,8 +736,8 @@ __global__ void __launch_bounds__(kRotThreads) few_rotate_kernel(const uint16_t*
 }
 
 // ---------------------------------------------------------------- joining and un-rotation
-// PER rows per warp, WARPS of them per block: o = R (sum_s 2^(m_s - m) acc_s) / l.  R^T (fp32) in shared memory, a lane
-// takes four output coordinates.
+// PER rows per warp, WARPS of them per block: o = R (sum_s 2^(m_s - m) acc_s) / l.  R^T (fp32) in
+// shared memory, a lane takes four output coordinates.
 struct JoinArgs {
     const float* part;
     const float2* ml;
