@@ -25,8 +25,9 @@
 //   1 sequence of 32768           32: 57, 103    64: 74, 107    128: 80, 108    256: 127, 117
 // 2048 queries of 4096 tokens (8192 rows), 513 and 131.  The average decides for the whole batch,
 // so a long piece among single tokens may go the slower way: 700 queries beside 31 single ones
-// over 2000 tokens each (91 rows on average), 240 and 195; 512 beside 31 over 4096 (68), 379 and
-// 342; 1000 beside 63 (66), 707 and 662.
+// over 2000 tokens each (91 rows on average), 240 and 195; 1000 beside 63 over 4096 (66), 707 and
+// 662; 800 beside 127 over 4096 (29), 937 and 1234; and where the long piece has most of the
+// tokens, 900 queries of 4096 beside 31 of 500 (116), 294 and 136.
 //
 // Roundings to fp16: R (one image of it, as the operand tiles leave no room for a second), the
 // levels (LevelTable) and the decompressed keys and values, which halves what the attention reads
